@@ -8,7 +8,9 @@ library is missing this module raises instead of computing anything.
 
 Functions keep the C names: qdelta_fwd, qed_fwd (with its ablation arms, the C
 qed_fwd_variant), qdelta_step, qed_step, qdelta_fwd_static_scratch,
-qdelta_workspace_bytes, qed_workspace_bytes, qd_device_status, qd_last_error.
+qdelta_workspace_bytes, qed_workspace_bytes, qd_device_status, qd_last_error.  The
+operators of the layer around a mixer (short_conv_*, ssm_*, group_norm_*) are bound in
+layer.py and exported here.
 """
 from __future__ import annotations
 
@@ -30,7 +32,10 @@ EXPORTS = ("qdelta_fwd", "qdelta_fwd_prologue", "qdelta_workspace_bytes", "qed_f
            "eda_fwd", "eda_workspace_bytes", "qd_device_status",
            "qd_selftest_bounded_wait",
            "qd_last_error",
-           "qd_last_launch_count")
+           "qd_last_launch_count",
+           "short_conv_fwd", "short_conv_step", "short_conv_bwd", "short_conv_bwd_workspace_bytes",
+           "ssm_fwd", "ssm_workspace_bytes", "ssm_step", "ssm_bwd", "ssm_bwd_workspace_bytes",
+           "group_norm_fwd", "group_norm_bwd", "group_norm_bwd_workspace_bytes")
 QED_VARIANTS = {"full": 0, "nogate": 1, "nogate_noproj": 2, "rand": 3}
 
 
@@ -83,6 +88,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qdelta_workspace_bytes.restype = Z
     lib.qed_workspace_bytes.restype = Z
     lib.qdelta_bwd_workspace_bytes.restype = Z
+    F = ctypes.c_float
+    lib.short_conv_fwd.argtypes = [P] * 7 + [I] * 6 + [P]
+    lib.short_conv_step.argtypes = [P] * 5 + [I] * 5 + [P]
+    lib.short_conv_bwd.argtypes = [P] * 11 + [I] * 6 + [P, Z, P]
+    lib.short_conv_bwd_workspace_bytes.argtypes = [I] * 5
+    lib.ssm_fwd.argtypes = [P] * 11 + [I] * 7 + [P, Z, P]
+    lib.ssm_workspace_bytes.argtypes = [I] * 6
+    lib.ssm_step.argtypes = [P] * 9 + [I] * 6 + [P]
+    lib.ssm_bwd.argtypes = [P] * 19 + [I] * 7 + [P, Z, P]
+    lib.ssm_bwd_workspace_bytes.argtypes = [I] * 6
+    lib.group_norm_fwd.argtypes = [P] * 5 + [I] * 3 + [F] + [I] * 3 + [P]
+    lib.group_norm_bwd.argtypes = [P] * 9 + [I] * 3 + [F] + [I] * 3 + [P, Z, P]
+    lib.group_norm_bwd_workspace_bytes.argtypes = [I] * 4
+    for f in (lib.short_conv_fwd, lib.short_conv_step, lib.short_conv_bwd, lib.ssm_fwd, lib.ssm_step, lib.ssm_bwd,
+              lib.group_norm_fwd, lib.group_norm_bwd):
+        f.restype = I
+    for f in (lib.short_conv_bwd_workspace_bytes, lib.ssm_workspace_bytes, lib.ssm_bwd_workspace_bytes,
+              lib.group_norm_bwd_workspace_bytes):
+        f.restype = Z
     lib.qd_last_error.restype = ctypes.c_char_p
     lib.qd_last_error.argtypes = []
     lib.qd_last_launch_count.argtypes = []
@@ -393,3 +417,8 @@ def qd_device_status(stream=None) -> int:
     """Synchronises the stream and returns the library's device status code."""
     dev = torch.cuda.current_device()
     return load_library().qd_device_status(_stream(stream, dev))
+
+
+from .layer import (group_norm_bwd, group_norm_bwd_workspace_bytes, group_norm_fwd, short_conv_bwd,  # noqa: E402
+                    short_conv_bwd_workspace_bytes, short_conv_fwd, short_conv_step, ssm_bwd, ssm_bwd_workspace_bytes,
+                    ssm_fwd, ssm_step, ssm_workspace_bytes)

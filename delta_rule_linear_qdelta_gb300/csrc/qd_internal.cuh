@@ -227,10 +227,81 @@ bool selftest_read_and_clear_timeout();
 
 // Records `msg` as this host thread's last error (qd_last_error) and returns `status`.
 qd_status report_error(qd_status status, const char *msg);
+// For entry points outside api.cu: clear the last error; record a success and its launches.
+void begin_call();
+qd_status end_call(int launches);
 // The host-side argument checks of qdelta_fwd (pointers, alignment, sizes, head
 // dims, chunk, dtype), without the workspace check; no CUDA call.
 qd_status check_qdelta_fwd_args(const char *fn, const void *q, const void *k, const void *v, const void *alpha,
                                 const void *beta, const void *lam, const float *S0, void *o, float *S_final,
                                 int B, int T, int H, int dk, int dv, int chunk, qd_dtype dtype);
+
+// Arguments of the short convolution (layouts as in include/qdelta.h); the step updates
+// S_final in place.
+struct ConvArgs {
+    const void *x;
+    const float *w, *bias;
+    const void *S0;
+    const int *lens;
+    void *y, *S_final;
+    int B, T, D, W, silu;
+};
+struct ConvBwdArgs {
+    const void *x;
+    const float *w, *bias;
+    const void *S0;
+    const int *lens;
+    const void *dy, *dS_final;
+    void *dx;
+    float *dw, *dbias;
+    void *dS0;
+    int B, T, D, W, silu;
+    float *part;      // the workspace: one row of [D][W] dw and [D] dbias per CTA along the tokens
+};
+
+// Arguments of the selective scan, its step (S_final in place, T = 1) and its backward.
+struct SsmArgs {
+    const void *x, *delta;
+    const float *A;
+    const void *Bm, *Cm;
+    const float *Dskip, *delta_bias, *S0;
+    const int *lens;
+    void *y;
+    float *S_final;
+    int B, T, D, G, N, softplus;
+    void *ws;
+    // backward
+    const void *dy;
+    const float *dS_final;
+    void *dx, *ddelta, *dB, *dC;
+    float *dA, *dD, *ddelta_bias, *dS0;
+};
+
+// Arguments of the group norm and its backward.
+struct NormArgs {
+    const void *x;
+    const float *w, *b;
+    const void *z;
+    void *y;
+    int M, H, d, center, silu;
+    float eps;
+    // backward
+    const void *dy;
+    void *dx, *dz;
+    float *dw, *db, *part;    // part: the workspace, or null when neither dw nor db is wanted
+};
+
+cudaError_t launch_conv_fwd(const ConvArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+cudaError_t launch_conv_step(const ConvArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+cudaError_t launch_conv_bwd(const ConvBwdArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+size_t conv_bwd_workspace(int B, int T, int D, int W);
+cudaError_t launch_ssm_fwd(const SsmArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+cudaError_t launch_ssm_step(const SsmArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+cudaError_t launch_ssm_bwd(const SsmArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+size_t ssm_fwd_workspace(int B, int T, int D, int G, int N);
+size_t ssm_bwd_workspace(int B, int T, int D, int G, int N);
+cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+cudaError_t launch_norm_bwd(const NormArgs &a, int dtype, cudaStream_t s, int *nlaunch);
+size_t norm_bwd_workspace(int M, int H, int d, int dtype);
 
 }  // namespace qd

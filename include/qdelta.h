@@ -1,6 +1,7 @@
 /*
  * qdelta.h -- C ABI of the GB300 (sm_103a) Q-Delta / QED / EDA forwards, the
- * Q-Delta backward and the decode steps.
+ * Q-Delta backward and the decode steps, and of the operators of the layer around
+ * them: short convolution, selective state space scan, group norm.
  *
  * Every entry point takes plain device pointers and sizes; no C++ or framework
  * types cross this boundary.  All device buffers are owned by the caller.  Every
@@ -283,6 +284,114 @@ QD_API qd_status eda_fwd(const void *q, const void *k, const void *v, const void
  * outputs ([B][T][H][128] each), the sub-tokens' bf16 strengths and one fp32 scalar per
  * token-head, each rounded up to 256 bytes; 0 otherwise. */
 QD_API size_t eda_workspace_bytes(int B, int T, int H, int dk, int dv, int chunk, qd_dtype dtype);
+
+/*
+ * The operators around the token mixers of this library: the short causal convolution
+ * before a recurrence, a diagonal selective state space scan as another recurrence, and
+ * the group norm with a gate after it.  Conventions for all of them:
+ *   D channels (H heads x d), tokens row-major and dense [B][T][D] in the call's dtype;
+ *   parameters and their gradients fp32; sums, statistics and states fp32.
+ *   lens [B] int32 on the device, or NULL (= T for all): tokens t >= lens[b] are padding
+ *   (values outside 0..T are clamped).  Their inputs are never used, whatever they hold;
+ *   their outputs and token gradients are written as 0; the state is the one after
+ *   lens[b] tokens.
+ *   Pointers are 16-byte aligned.  Any D; B, T may be 0.  Results do not depend on the run:
+ *   sums over tokens and channels are taken in a fixed order.
+ *   No output may alias an input, but S_final may be S0 (in-place carry).
+ */
+
+/*
+ * short_conv_fwd -- depthwise causal convolution with W taps (2, 3 or 4), per channel:
+ *     pre_t = bias + sum_{j < W} w[j] x_{t-W+1+j},   y_t = silu ? SiLU(pre_t) : pre_t
+ *   w [D][W] fp32, bias [D] fp32 or NULL (= 0)
+ *   S0, S_final [B][W-1][D] in the call's dtype: the W - 1 inputs before the call (NULL = 0),
+ *   and the last W - 1 inputs after it (NULL: not written)
+ */
+QD_API qd_status short_conv_fwd(const void *x, const float *w, const float *bias, const void *S0, const int *lens,
+                                void *y, void *S_final, int B, int T, int D, int W, int silu, qd_dtype dtype,
+                                cudaStream_t stream);
+
+/* short_conv_step -- one token for each of N sequences: x, y [N][D]; S [N][W-1][D], the last
+ * W - 1 inputs, is updated in place. */
+QD_API qd_status short_conv_step(void *S, const void *x, const float *w, const float *bias, void *y, int N, int D, int W,
+                                 int silu, qd_dtype dtype, cudaStream_t stream);
+
+/*
+ * short_conv_bwd -- gradients of sum(dy * y) + sum(dS_final * S_final) for short_conv_fwd.
+ * Inputs as passed to it; dS_final [B][W-1][D] in the call's dtype or NULL (= 0).
+ * Outputs, each overwritten: dx [B][T][D], dw [D][W] fp32 (required); dbias [D] fp32 and
+ * dS0 [B][W-1][D] in the call's dtype when non-NULL.
+ * workspace: at least short_conv_bwd_workspace_bytes(...) bytes.
+ */
+QD_API qd_status short_conv_bwd(const void *x, const float *w, const float *bias, const void *S0, const int *lens,
+                                const void *dy, const void *dS_final, void *dx, float *dw, float *dbias, void *dS0,
+                                int B, int T, int D, int W, int silu, qd_dtype dtype, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+QD_API size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int W, qd_dtype dtype);
+
+/*
+ * ssm_fwd -- selective state space scan with a diagonal state of N per channel (1..128).  Per
+ * channel d of group g = d / (D / G), n < N:
+ *     u_t = softplus(delta_t + delta_bias)      (softplus = 0: the sum itself)
+ *     h_t[n] = exp(u_t A[d][n]) h_{t-1}[n] + u_t x_t B_t[g][n]
+ *     y_t = sum_n C_t[g][n] h_t[n] + Dskip x_t
+ *   x, delta, y [B][T][D]; B, C [B][T][G][N] in the call's dtype; A [D][N], Dskip [D],
+ *   delta_bias [D] fp32 (the last two NULL = 0); G divides D
+ *   S0, S_final [B][D][N] fp32 (the state format of this library with d_v rows of N): NULL = 0,
+ *   NULL = not written
+ * A < 0 is expected (a decay); other values are computed as written.
+ * workspace: at least ssm_workspace_bytes(...) bytes (0, then NULL is fine, unless few channels
+ * carry many tokens, which are then cut into segments).
+ */
+QD_API qd_status ssm_fwd(const void *x, const void *delta, const float *A, const void *Bm, const void *Cm,
+                         const float *Dskip, const float *delta_bias, const float *S0, const int *lens, void *y,
+                         float *S_final, int B, int T, int D, int G, int N, int softplus, qd_dtype dtype,
+                         void *workspace, size_t workspace_bytes, cudaStream_t stream);
+QD_API size_t ssm_workspace_bytes(int B, int T, int D, int G, int N, qd_dtype dtype);
+
+/* ssm_step -- one token for each of Nseq sequences: x, delta, y [Nseq][D], B, C [Nseq][G][N];
+ * the state S [Nseq][D][N] fp32 is read once and updated in place. */
+QD_API qd_status ssm_step(float *S, const void *x, const void *delta, const float *A, const void *Bm, const void *Cm,
+                          const float *Dskip, const float *delta_bias, void *y, int Nseq, int D, int G, int N,
+                          int softplus, qd_dtype dtype, cudaStream_t stream);
+
+/*
+ * ssm_bwd -- gradients of sum(dy * y) + sum(dS_final * S_final) for ssm_fwd.  Inputs as passed to
+ * it; dy [B][T][D] in the call's dtype, dS_final [B][D][N] fp32 or NULL (= 0).
+ * Outputs, each overwritten: dx, ddelta [B][T][D] and dB, dC [B][T][G][N] in the call's dtype
+ * (ddelta: of the raw delta), dA [D][N] fp32 (required); dDskip [D] and ddelta_bias [D] fp32
+ * when non-NULL and the parameter is; dS0 [B][D][N] fp32 when non-NULL (also when S0 is NULL).
+ * workspace: at least ssm_bwd_workspace_bytes(...) bytes (the state entering every 16 tokens,
+ * and partial sums).
+ */
+QD_API qd_status ssm_bwd(const void *x, const void *delta, const float *A, const void *Bm, const void *Cm,
+                         const float *Dskip, const float *delta_bias, const float *S0, const int *lens,
+                         const void *dy, const float *dS_final, void *dx, void *ddelta, float *dA, void *dBm, void *dCm,
+                         float *dDskip, float *ddelta_bias, float *dS0, int B, int T, int D, int G, int N, int softplus,
+                         qd_dtype dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+QD_API size_t ssm_bwd_workspace_bytes(int B, int T, int D, int G, int N, qd_dtype dtype);
+
+/*
+ * group_norm_fwd -- group norm of each token's channels with an activation or a gate: x, y, z
+ * [M][H][d] (M tokens, H groups of d <= 8192 channels; H = 1 normalises whole rows).  Per group:
+ *     xh = (x - mean) / sqrt(var + eps)       center = 0: x / sqrt(mean(x^2) + eps)
+ *     n = xh w + b                            w, b [H][d] fp32 (NULL: 1, 0)
+ *     y = act(n), or n act(z) with a gate z   act: SiLU when silu, else the identity
+ * eps must be positive.
+ */
+QD_API qd_status group_norm_fwd(const void *x, const float *w, const float *b, const void *z, void *y, int M, int H,
+                                int d, float eps, int center, int silu, qd_dtype dtype, cudaStream_t stream);
+
+/*
+ * group_norm_bwd -- gradients of sum(dy * y) for group_norm_fwd: dx (required) and dz (required
+ * when z is given) [M][H][d] in the call's dtype; dw, db [H][d] fp32 when non-NULL and the
+ * parameter is.  workspace: at least group_norm_bwd_workspace_bytes(...) bytes when dw or db is
+ * wanted.
+ */
+QD_API qd_status group_norm_bwd(const void *x, const float *w, const float *b, const void *z, const void *dy, void *dx,
+                                void *dz, float *dw, float *db, int M, int H, int d, float eps, int center, int silu,
+                                qd_dtype dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+QD_API size_t group_norm_bwd_workspace_bytes(int M, int H, int d, qd_dtype dtype);
 
 /*
  * qdelta_fwd_static_scratch -- qdelta_fwd for callers that cannot allocate device
