@@ -116,22 +116,33 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
             if (a.b) load_param<VEC>(a.b + (size_t)at.h * a.d + at.c[k], b[k]);
         }
     }
+    const int64_t first = (int64_t)(blockIdx.x / p.nhb) * p.MB, turn = (int64_t)p.gm * p.MB;
+    Pack<T, VEC> x[K], z[K], xn[K], zn[K];
+    auto fetch = [&](int64_t m) {
+        const size_t row = ((size_t)m * a.H + at.h) * a.d;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            xn[k].zero();
+            zn[k].zero();
+            if (at.on[k] && m < a.M) {
+                xn[k].load((const T *)a.x + row + at.c[k]);
+                if (a.z) zn[k].load((const T *)a.z + row + at.c[k]);
+            }
+        }
+    };
+    fetch(first + at.ml);
     // every thread of the CTA makes the same number of turns: the group totals synchronise
-    for (int64_t m0 = (int64_t)(blockIdx.x / p.nhb) * p.MB; m0 < a.M; m0 += (int64_t)p.gm * p.MB) {
+    for (int64_t m0 = first; m0 < a.M; m0 += turn) {
         const int64_t m = m0 + at.ml;
         const size_t row = ((size_t)m * a.H + at.h) * a.d;
-        Pack<T, VEC> x[K], z[K];
         float v[K][VEC];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            x[k].zero();
-            z[k].zero();
-            if (at.on[k] && m < a.M) {
-                x[k].load((const T *)a.x + row + at.c[k]);
-                if (a.z) z[k].load((const T *)a.z + row + at.c[k]);
-            }
+            x[k] = xn[k];
+            z[k] = zn[k];
             x[k].get(v[k]);
         }
+        fetch(m + turn);                               // the next token's, while this one is computed
         normalise<VEC, K>(v, at.on, a.d, a.center, a.eps, p.lpg, sm);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -171,23 +182,35 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
         }
     }
     const float inv_d = 1.f / (float)a.d;
-    for (int64_t m0 = (int64_t)(blockIdx.x / p.nhb) * p.MB; m0 < a.M; m0 += (int64_t)p.gm * p.MB) {
+    const int64_t begin = (int64_t)(blockIdx.x / p.nhb) * p.MB, turn = (int64_t)p.gm * p.MB;
+    Pack<T, VEC> x[K], z[K], dy[K], xn[K], zn[K], dyn[K];
+    auto fetch = [&](int64_t m) {
+        const size_t row = ((size_t)m * a.H + at.h) * a.d;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            xn[k].zero();
+            zn[k].zero();
+            dyn[k].zero();
+            if (at.on[k] && m < a.M) {
+                xn[k].load((const T *)a.x + row + at.c[k]);
+                dyn[k].load((const T *)a.dy + row + at.c[k]);
+                if (a.z) zn[k].load((const T *)a.z + row + at.c[k]);
+            }
+        }
+    };
+    fetch(begin + at.ml);
+    for (int64_t m0 = begin; m0 < a.M; m0 += turn) {
         const int64_t m = m0 + at.ml;
         const size_t row = ((size_t)m * a.H + at.h) * a.d;
-        Pack<T, VEC> x[K], z[K], dy[K];
         float v[K][VEC];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            x[k].zero();
-            z[k].zero();
-            dy[k].zero();
-            if (at.on[k] && m < a.M) {
-                x[k].load((const T *)a.x + row + at.c[k]);
-                dy[k].load((const T *)a.dy + row + at.c[k]);
-                if (a.z) z[k].load((const T *)a.z + row + at.c[k]);
-            }
+            x[k] = xn[k];
+            z[k] = zn[k];
+            dy[k] = dyn[k];
             x[k].get(v[k]);
         }
+        fetch(m + turn);
         const float rstd = normalise<VEC, K>(v, at.on, a.d, a.center, a.eps, p.lpg, sm);
         float s1 = 0.f, s2 = 0.f, g[K][VEC];
 #pragma unroll

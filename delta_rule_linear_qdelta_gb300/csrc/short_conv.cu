@@ -14,7 +14,7 @@ namespace qd {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;             // tokens loaded before the first of them is used
+constexpr int kBatch = 4;             // tokens in flight while as many are computed
 
 // `rows` consecutive channels' filters, w[c * W + j]; 16-byte loads when VEC > 1.
 template <int VEC, int W> __device__ __forceinline__ void load_filter(const float *w, float (&f)[VEC][W]) {
@@ -75,13 +75,19 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int run,
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) head[k].get(win[k + 1]);
 
-    for (int t = t0; t < t1; t += kBatch) {
-        P in[kBatch];
+    P in[kBatch], next[kBatch];
+    auto fetch = [&](P(&to)[kBatch], int t) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            in[u].zero();
-            if (t + u < t1 && t + u < n) in[u].load(x + (size_t)(t + u) * D);
+            to[u].zero();
+            if (t + u < t1 && t + u < n) to[u].load(x + (size_t)(t + u) * D);
         }
+    };
+    fetch(next, t0);
+    for (int t = t0; t < t1; t += kBatch) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) in[u] = next[u];
+        fetch(next, t + kBatch);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
@@ -207,17 +213,26 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(ConvBwdArgs a, in
             v.get(win[k + 1]);
         }
         const int end = t1 + W - 1;                    // tokens t1 .. end - 1 complete the run's last dx
-        for (int t = t0; t < end; t += kBatch) {
-            P xi[kBatch], gi[kBatch];
+        P xi[kBatch], gi[kBatch], xn[kBatch], gn[kBatch];
+        auto fetch = [&](int t) {
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                xi[u].zero();
-                gi[u].zero();
+                xn[u].zero();
+                gn[u].zero();
                 if (t + u < end && t + u < n) {
-                    xi[u].load(x + (size_t)(t + u) * D);
-                    gi[u].load(dy + (size_t)(t + u) * D);
+                    xn[u].load(x + (size_t)(t + u) * D);
+                    gn[u].load(dy + (size_t)(t + u) * D);
                 }
             }
+        };
+        fetch(t0);
+        for (int t = t0; t < end; t += kBatch) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                xi[u] = xn[u];
+                gi[u] = gn[u];
+            }
+            fetch(t + kBatch);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int tt = t + u;

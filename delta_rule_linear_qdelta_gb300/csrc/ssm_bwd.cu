@@ -1,4 +1,4 @@
-// Backward of the selective state space scan (ssm_fwd.cu has the forward's formulas).  With
+// Backward of the selective state space scan (ssm_scan.cuh has the forward's formulas).  With
 // g = dy and the gradient dh_t of L with respect to h_t,
 //
 //   dh_t = C_t g_t + a_{t+1} dh_{t+1}   (+ dS_final at the last token),   r_t = dh_t a_t h_{t-1}
@@ -6,28 +6,30 @@
 //   dA = sum_{b,t} u r,  dB = sum_d dh u x,  dC = sum_d g h,  dD = sum g x,  dS0 = a_1 dh_1
 //
 // Launches:
-//  1. states: the forward recurrence again, which leaves the state entering every chunk of 16
-//     tokens in the workspace (4 bytes per token and channel at N = 16).  Few channels over
-//     many tokens: the tokens are cut into segments as in the forward; each starts from zero
-//     and also leaves its end E, its sum of u and R, the gradient that its own tokens send to
-//     the state entering it, R = sum_t (prod_{s<=t} a_s) C_t g_t.
-//  2. gradients: a CTA walks its segment's chunks backwards.  Per chunk it recomputes the 16
+//  1. the forward recurrence again, leaving the state entering every chunk of 8 tokens in the
+//     workspace (8 bytes per token and channel at N = 16).  Few channels over many tokens: the
+//     tokens are cut into segments as in the forward; each starts from zero and also leaves its
+//     end E, its sum of u and R, the gradient that its own tokens send to the state entering it,
+//     R = sum_t (prod_{s<=t} a_s) C_t g_t.
+//  2. gradients: a CTA walks its segment's chunks backwards.  Per chunk it recomputes the 8
 //     states into registers from the checkpoint, then runs dh down the tokens.  Sums over n
 //     join over the LN lanes of a channel; sums over channels (dB, dC) over the channels of a
 //     warp by shuffles, over the CTA's warps through shared memory.
 //  3. the sums over CTAs: dB, dC over the channel blocks, and dA, dD, d bias over sequences
 //     and segments; in a fixed order, so results do not change from run to run.
-// Bound by instruction issue: two exponentials and about 20 operations per (token, channel,
-// state) in launch 2, one and 4 in launch 1.
+// Bound by instruction issue and the shared-memory pipe: two exponentials and about 20
+// operations per (token, channel, state) in launch 2, one and 4 in launch 1.
+#include <limits.h>
+
 #include "layer_common.cuh"
-#include "ssm_tile.cuh"
+#include "ssm_scan.cuh"
 
 namespace qd {
 namespace {
 
 using namespace ssm;
 
-constexpr int kChunk = 16;            // tokens between checkpoints
+constexpr int kGradThreads = 128, kGradWarps = kGradThreads / 32, kSumThreads = 256;
 
 // Everything in the workspace, in floats from its start.
 struct BwdWs {
@@ -37,14 +39,17 @@ struct BwdWs {
     size_t chk, ucum, E, U, R, dbc, par, total;
 };
 
-__host__ __device__ constexpr int bwd_lanes(int N) { return padded_states(N) / 4; }
+__host__ __device__ constexpr int grad_lanes(int N) { return padded_states(N) / 4; }
+__host__ __device__ constexpr int grad_channels(int N) { return 2 * kGradThreads / grad_lanes(N); }
 
 BwdWs bwd_ws(int B, int T, int D, int G, int N) {
     BwdWs w;
     const size_t NP = padded_states(N), bd = (size_t)B * D;
-    const int CPB = kThreads / bwd_lanes(N);
-    w.nb = channel_blocks(D, G, CPB) / G;
-    w.sp = split_tokens((int64_t)B * G * w.nb, T, kSMs, 2 * kSMs, 2 * kTile);
+    w.nb = channel_blocks(D, G, grad_channels(N)) / G;
+    // One segment when the CTAs fill every SM's three places; otherwise two rounds of them: one
+    // round is 3 % faster at equal lengths, two are 17 % faster at ragged ones (4 x 4096 x 1024 and
+    // 3 x 517 x 770 channels).
+    w.sp = split_tokens((int64_t)B * G * w.nb, T, 3 * kSMs, 6 * kSMs, 4 * kTile);
     w.nck = (T + kChunk - 1) / kChunk;
     w.rows = B * w.sp.S;
     const bool multi = w.sp.S > 1;
@@ -61,330 +66,338 @@ BwdWs bwd_ws(int B, int T, int D, int G, int N) {
     return w;
 }
 
-__device__ __forceinline__ void put4(float *p, const float *v) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
-__device__ __forceinline__ void get4(const float *p, float *v) {
-    const float4 f = *reinterpret_cast<const float4 *>(p);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-}
-
-// Launch 1.  Geometry as in the forward.
-template <typename T, int LN, int SPL, bool WIDE, bool MULTI>
-__global__ void __launch_bounds__(kThreads) states_kernel(SsmArgs a, BwdWs w, float *ws) {
-    using G = Geo<T, LN, SPL, WIDE>;
-    constexpr int CPB = G::CPB, NP = G::NP;
-    extern __shared__ float smem[];
-    float2 *su = reinterpret_cast<float2 *>(smem);                     // [kTile][CPB] (u, u x)
-    float *sB = smem + 2 * kTile * CPB;                                // [kTile][NP]
-    float *sC = sB + kTile * NP;                                       // [kTile][NP], MULTI
-    float *sg = sC + kTile * NP;                                       // [kTile][CPB] dy, MULTI
-
-    const int tid = threadIdx.x, ln = tid % LN, ch = tid / LN, seg = blockIdx.y;
-    const int nblk = channel_blocks(a.D, a.G, CPB), b = blockIdx.x / nblk;
-    const ChannelBlock cb(a, blockIdx.x % nblk, CPB);
-    const int D = a.D, N = a.N, d = cb.first + ch;
-    const bool live = ch < cb.count;
-    const int n = seq_len(a.lens, b, a.T);
-    const int t_begin = seg * w.sp.len, t_end = min(min(t_begin + w.sp.len, a.T), n);
-    const size_t bd = (size_t)b * D + d, all = (size_t)a.B * D;
-
-    float A2[SPL], h[SPL], P[SPL], R[SPL], U = 0.f;
-#pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        const bool on = live && ln * SPL + i < N;
-        A2[i] = on ? a.A[(size_t)d * N + ln * SPL + i] * kLog2e : 0.f;
-        h[i] = on && seg == 0 && a.S0 ? a.S0[bd * N + ln * SPL + i] : 0.f;
-        P[i] = 1.f;
-        R[i] = 0.f;
-    }
-    typename G::Stage st;
-    if (t_begin < t_end) st.load(a, cb, b, t_begin, n, MULTI);
-    for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
-        st.store_tokens(a, cb, t0, n, su);
-        st.store_groups(a, cb, b, t0, n, sB, sC, MULTI);
-        if (MULTI) {
-            for (int e = tid; e < kTile * G::ROW; e += kThreads) {
-                const int t = e / G::ROW, c = e % G::ROW * G::VEC;
-                typename G::Vec v;
-                v.zero();
-                if (t0 + t < n && c < cb.count) v.load((const T *)a.dy + ((size_t)b * a.T + t0 + t) * D + cb.first + c);
-                float f[G::VEC];
-                v.get(f);
-#pragma unroll
-                for (int k = 0; k < G::VEC; ++k) sg[t * CPB + c + k] = f[k];
-            }
-        }
-        __syncthreads();
-        if (t0 + kTile < t_end) st.load(a, cb, b, t0 + kTile, n, MULTI);
-#pragma unroll 1
-        for (int c0 = 0; c0 < kTile && t0 + c0 < t_end; c0 += kChunk) {
-            const size_t ck = (size_t)((t0 + c0) / kChunk) * all + bd;
-            if (live) {
-#pragma unroll
-                for (int i = 0; i < SPL; i += 4) put4(ws + w.chk + ck * NP + ln * SPL + i, h + i);
-                if (MULTI && ln == 0) ws[w.ucum + ck] = U;
-            }
-#pragma unroll 4
-            for (int t = c0; t < c0 + kChunk; ++t) {
-                const float2 uu = su[t * CPB + ch];
-                const float g = MULTI ? sg[t * CPB + ch] : 0.f;
-                if (MULTI) U += uu.x;
-#pragma unroll
-                for (int i = 0; i < SPL; i += 4) {
-                    float Bf[4], Cf[4];
-                    get4(sB + t * NP + ln * SPL + i, Bf);
-                    if (MULTI) get4(sC + t * NP + ln * SPL + i, Cf);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float av = exp2_fast(uu.x * A2[i + k]);
-                        h[i + k] = fmaf(av, h[i + k], uu.y * Bf[k]);
-                        if (MULTI) {
-                            P[i + k] *= av;
-                            R[i + k] = fmaf(P[i + k], g * Cf[k], R[i + k]);
-                        }
-                    }
-                }
-            }
-        }
-        __syncthreads();
-    }
-    if (MULTI && live) {
-        const size_t at = seg * all + bd;
-#pragma unroll
-        for (int i = 0; i < SPL; i += 4) {
-            put4(ws + w.E + at * NP + ln * SPL + i, h + i);
-            put4(ws + w.R + at * NP + ln * SPL + i, R + i);
-        }
-        if (ln == 0) ws[w.U + at] = U;
-    }
-}
-
-// Launch 2.  LN lanes by four states per channel.
+// Launch 2.  A thread holds 2 channels by 4 states, LN lanes share a channel pair, CL = 32 / LN
+// pairs make a warp.  dB and dC of a token are sums over the warp's channels of 4 states each:
+// they are joined like lane_reduce, but a lane keeps its four states in the order n ^ m, m two
+// of its channel bits, so what it gives away is always its upper half and nothing has to be
+// selected; B and C lie in shared memory in all four orders.
 template <typename T, int LN, bool WIDE>
-__global__ void __launch_bounds__(kThreads) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
-    constexpr int CPB = kThreads / LN, NP = 4 * LN, CL = 32 / LN;      // CL channels a warp
-    constexpr int VEC = WIDE ? 4 : 1, ROW = CPB / VEC, PER = (kChunk * ROW + kThreads - 1) / kThreads;
-    constexpr int TB = LN < 4 ? LN : 4;                                // tokens whose sums over n join at once
-    constexpr int OS = CPB + CL;                                       // row of the outputs, padded
-    using Vec = Pack<T, VEC>;
-    extern __shared__ float smem[];
-    float4 *sp = reinterpret_cast<float4 *>(smem);                     // [kChunk][CPB] (u, x, g, softplus')
-    float2 *so = reinterpret_cast<float2 *>(smem + 4 * kChunk * CPB);  // [kChunk][OS] (dx, ddelta)
-    float *sB = smem + 4 * kChunk * CPB + 2 * kChunk * OS;             // [kChunk][NP]
-    float *sC = sB + kChunk * NP;
-    float *sr = sC + kChunk * NP;                                      // [8 warps][kChunk][2 NP] (dB, dC)
+__global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
+    constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN, CL = 32 / LN;
+    constexpr int TB = LN >= 4 ? 2 : 1, CNT = 2 * TB;                  // tokens whose sums over n join at once
+    using St = Staging<T, kGradThreads, CPB, NP, 3, WIDE>;
+    constexpr int VEC = St::VEC, PER = St::PER;
+    extern __shared__ float4 smem4[];
+    T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
+    float4 *su = smem4 + St::BYTES / 16;                                                // [kTile][PAIRS] (u0, u1, u0 x0, u1 x1)
+    float2 *sx = reinterpret_cast<float2 *>(su + kTile * PAIRS);       // [kTile][CPB] (x, softplus')
+    float2 *so = sx + kTile * CPB;                                     // [kTile][CPB] (dx, ddelta)
+    float2 *sg = so + kTile * CPB;                                     // [kTile][PAIRS] (g0, g1)
+    float *sB = reinterpret_cast<float *>(sg + kTile * PAIRS);         // [4 orders][kTile][NP]
+    float *sC = sB + 4 * kTile * NP;
+    float *sr = sC + 4 * kTile * NP;                                   // [warps][kTile][2 NP] (dB, dC)
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = tid % LN, ch = tid / LN, seg = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = tid % LN, pr = tid / LN, seg = blockIdx.y;
+    const int cl = lane / LN, m = (CL >= 2 ? (cl & 1) * 2 : 0) + (CL >= 4 ? cl >> 1 & 1 : 0);
     const int nblk = channel_blocks(a.D, a.G, CPB), b = blockIdx.x / nblk, blk = blockIdx.x % nblk;
     const ChannelBlock cb(a, blk, CPB);
-    const int D = a.D, N = a.N, d = cb.first + ch, S = w.sp.S;
-    const bool live = ch < cb.count;
+    const int D = a.D, N = a.N, S = w.sp.S, c0 = 2 * pr;
     const int n = seq_len(a.lens, b, a.T);
     const int t_begin = seg * w.sp.len, t_stop = min(t_begin + w.sp.len, a.T), t_end = min(t_stop, n);
-    const size_t bd = (size_t)b * D + d, all = (size_t)a.B * D;
-    const float Dsk = live && a.Dskip ? a.Dskip[d] : 0.f;
+    const size_t bd = (size_t)b * D + cb.first + c0, all = (size_t)a.B * D;
 
-    float A2[4], dh[4], dA[4], hin[4];                                 // dh: what reaches the state from the right
+    // four states of a channel in the lane's order
+    auto order = [&](float4 v, f32x2(&to)[2]) {
+        if (m & 2) v = make_float4(v.z, v.w, v.x, v.y);
+        if (m & 1) v = make_float4(v.y, v.x, v.w, v.z);
+        to[0] = pk(v.x, v.y);
+        to[1] = pk(v.z, v.w);
+    };
+    // a parameter or state [.., N] of channel c, by single accesses: once per segment
+    auto gather = [&](const float *base, size_t row, int c, f32x2(&to)[2]) {
+        float f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool on = live && ln * 4 + i < N;
-        A2[i] = on ? a.A[(size_t)d * N + ln * 4 + i] * kLog2e : 0.f;
-        dh[i] = on && a.dS_final ? a.dS_final[bd * N + ln * 4 + i] : 0.f;
-        dA[i] = hin[i] = 0.f;
-    }
-    float dDs = 0.f, dbs = 0.f;
-    if (S > 1 && live) {
-        for (int s = S - 1; s > seg; --s) {
-            const float U = ws[w.U + s * all + bd];
-            float r[4];
-            get4(ws + w.R + (s * all + bd) * NP + ln * 4, r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dh[i] = fmaf(exp2_fast(U * A2[i]), dh[i], r[i]);
+        for (int i = 0; i < 4; ++i) {
+            const int k = ln * 4 + (i ^ m);
+            f[i] = base && c0 + c < cb.count && k < N ? base[row * N + k] : 0.f;
         }
-        for (int s = 0; s < seg; ++s) {
-            const float U = ws[w.U + s * all + bd];
-            float e[4];
-            get4(ws + w.E + (s * all + bd) * NP + ln * 4, e);
+        to[0] = pk(f[0], f[1]);
+        to[1] = pk(f[2], f[3]);
+    };
+    auto scatter = [&](float *base, size_t row, int c, const f32x2(&v)[2]) {
+        float f[4];
+        unpk(v[0], f[0], f[1]);
+        unpk(v[1], f[2], f[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) hin[i] = fmaf(exp2_fast(U * A2[i]), hin[i], e[i]);
-        }
-    }
-
-    Vec xr[PER], dr[PER], gr[PER];
-    auto load = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = tid + i * kThreads, t = e / ROW, c = e % ROW * VEC;
-            xr[i].zero();
-            dr[i].zero();
-            gr[i].zero();
-            if (t < kChunk && t0 + t < n && c < cb.count) {
-                const size_t at = ((size_t)b * a.T + t0 + t) * D + cb.first + c;
-                xr[i].load((const T *)a.x + at);
-                dr[i].load((const T *)a.delta + at);
-                gr[i].load((const T *)a.dy + at);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int k = ln * 4 + (i ^ m);
+            if (c0 + c < cb.count && k < N) base[row * N + k] = f[i];
         }
     };
-    const int chunks = t_begin < t_end ? (t_end - t_begin + kChunk - 1) / kChunk : 0;
-    if (chunks) load(t_begin + (chunks - 1) * kChunk);
-    for (int c = chunks - 1; c >= 0; --c) {
-        const int t0 = t_begin + c * kChunk;
-        // stage the chunk
+    // the same of a workspace array [.., NP]
+    auto fetch = [&](size_t base, size_t row, int c, f32x2(&to)[2]) {
+        order(*reinterpret_cast<const float4 *>(ws + base + (row + c) * NP + ln * 4), to);
+    };
+
+    f32x2 A2[2][2], dh[2][2], dA[2][2], hin[2][2];                     // A log2(e); dh: what reaches the state from the right
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        gather(a.A, cb.first + c0 + c, c, A2[c]);
+        gather(a.dS_final, bd + c, c, dh[c]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            A2[c][p] = mul2(A2[c][p], pk(kLog2e, kLog2e));
+            dA[c][p] = hin[c][p] = 0;
+        }
+        if (S > 1 && c0 + c < cb.count) {
+            for (int s = S - 1; s > seg; --s) {
+                const float U = ws[w.U + s * all + bd + c];
+                f32x2 r[2];
+                fetch(w.R, s * all + bd, c, r);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) dh[c][p] = fma2(exp2_2(mul2(pk(U, U), A2[c][p])), dh[c][p], r[p]);
+            }
+            for (int s = 0; s < seg; ++s) {
+                const float U = ws[w.U + s * all + bd + c];
+                f32x2 e[2];
+                fetch(w.E, s * all + bd, c, e);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) hin[c][p] = fma2(exp2_2(mul2(pk(U, U), A2[c][p])), hin[c][p], e[p]);
+            }
+        }
+    }
+    // the (token, channel) of a batch whose sums over n this lane ends up with
+    const int mine = reduced_first<CNT, LN, 1>(lane), myk = mine / 2, myc = mine & 1;
+    const bool owner = reduced_owner<CNT, LN, 1>(lane);
+    const float Dsk = a.Dskip && c0 + myc < cb.count ? a.Dskip[cb.first + c0 + myc] : 0.f;
+    float dDs = 0.f, dbs = 0.f;
+
+    float bias[VEC];
+    if (St::FIXED) St::param(a.delta_bias, cb, 0, bias);
+    const int tiles = t_begin < t_end ? (t_end - t_begin + kTile - 1) / kTile : 0;
+    // the tile-th tile of the segment, none (and no copies) before the first
+    auto issue = [&](int tile, int buf) {
+        St::issue(raw, buf, a, cb, b, t_begin + tile * kTile, tile >= 0 ? t_end : INT_MIN, n, true, {a.x, a.delta, a.dy});
+    };
+    issue(tiles - 1, 0);
+    issue(tiles - 2, 1);
+    // the checkpoint of the next chunk is on its way while one is computed
+    float4 ck_h[2];
+    float ck_u[2];
+    auto checkpoint = [&](int t) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const size_t row = (size_t)(t / kChunk) * all + (size_t)b * D + cb.first + min(c0 + c, cb.count - 1);
+            ck_h[c] = *reinterpret_cast<const float4 *>(ws + w.chk + row * NP + ln * 4);
+            if (S > 1) ck_u[c] = ws[w.ucum + row];
+        }
+    };
+    if (tiles) checkpoint(t_begin + (t_end - 1 - t_begin) / kChunk * kChunk);
+    int buf = 0;
+    for (int tile = tiles - 1; tile >= 0; --tile, buf = buf + 1 < kStages ? buf + 1 : 0) {
+        const int t0 = t_begin + tile * kTile;
+        issue(tile - 2, buf + 2 < kStages ? buf + 2 : buf + 2 - kStages);
+        if constexpr (WIDE) copies_done<2>();
+        const bool full = St::full(cb, t0, n);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = tid + i * kThreads, t = e / ROW, cc = e % ROW * VEC;
-            if (t >= kChunk) break;
-            float xf[VEC], df[VEC], gf[VEC];
-            xr[i].get(xf);
-            dr[i].get(df);
-            gr[i].get(gf);
+            const int t = St::tok(i), c = St::chan(i);
+            if (t >= kTile) break;
+            float u[VEC], x[VEC], g[VEC], sig[VEC];
+            if (!St::FIXED) St::param(a.delta_bias, cb, i, bias);
+            St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
+            St::get(raw, buf, 1, i, a, cb, b, t0, n, a.delta, u);
+            St::get(raw, buf, 2, i, a, cb, b, t0, n, a.dy, g);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                float u = 0.f, sig = 0.f;
-                if (t0 + t < n && cc + k < cb.count) {
-                    u = df[k] + (a.delta_bias ? a.delta_bias[cb.first + cc + k] : 0.f);
-                    sig = 1.f;
-                    if (a.softplus) u = softplus_grad_f(u, sig);
+            for (int k = 0; k < VEC; k += 2) {
+                float e0 = 0.f, e1 = 0.f, none = 0.f, &u1 = k + 1 < VEC ? u[k + 1 < VEC ? k + 1 : k] : none;
+                u[k] += bias[k];
+                if (k + 1 < VEC) u1 += bias[k + 1 < VEC ? k + 1 : k];
+                const float r0 = u[k], r1 = u1;
+                if (a.softplus) softplus2(u[k], u1, e0, e1);
+                sig[k] = a.softplus ? softplus_grad(r0, e0) : 1.f;
+                if (k + 1 < VEC) sig[k + 1 < VEC ? k + 1 : k] = a.softplus ? softplus_grad(r1, e1) : 1.f;
+            }
+            if (!full && !(t0 + t < n && c < cb.count)) {              // of the padding nothing counts
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) u[k] = 0.f;
+            }
+            if constexpr (VEC == 4) {
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    su[t * PAIRS + (c + k) / 2] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
+                    sg[t * PAIRS + (c + k) / 2] = make_float2(g[k], g[k + 1]);
+                    *reinterpret_cast<float4 *>(sx + t * CPB + c + k) = make_float4(x[k], sig[k], x[k + 1], sig[k + 1]);
                 }
-                sp[t * CPB + cc + k] = make_float4(u, xf[k], gf[k], sig);
+            } else {
+                float *to = reinterpret_cast<float *>(su + t * PAIRS + c / 2) + (c & 1);
+                to[0] = u[0];
+                to[2] = u[0] * x[0];
+                reinterpret_cast<float *>(sg + t * PAIRS + c / 2)[c & 1] = g[0];
+                sx[t * CPB + c] = make_float2(x[0], sig[0]);
             }
         }
-        for (int e = tid; e < 2 * kChunk * NP; e += kThreads) {
-            const int which = e / (kChunk * NP), r = e % (kChunk * NP), t = r / NP, k = r % NP;
-            float f = 0.f;
-            if (t0 + t < n && k < N)
-                f = to_f(((const T *)(which ? a.Cm : a.Bm))[(((size_t)b * a.T + t0 + t) * a.G + cb.group) * N + k]);
-            sB[e] = f;
-        }
-        float h0[4] = {0.f, 0.f, 0.f, 0.f};
-        if (live) {
-            const size_t ck = (size_t)(t0 / kChunk) * all + bd;
-            get4(ws + w.chk + ck * NP + ln * 4, h0);
-            if (seg > 0) {
-                const float U = ws[w.ucum + ck];
+        St::get_groups(raw, buf, a, cb, b, t0, n, true, [&](int which, int t, int k, const float (&f)[4]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h0[i] = fmaf(exp2_fast(U * A2[i]), hin[i], h0[i]);
-            }
-        }
+            for (int o = 0; o < 4; ++o)
+                *reinterpret_cast<float4 *>((which ? sC : sB) + (o * kTile + t) * NP + k) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
+        });
         __syncthreads();
-        if (c > 0) load(t0 - kChunk);
 
-        float hh[kChunk][4];
+#pragma unroll 1
+        for (int tc = kTile - kChunk; tc >= 0; tc -= kChunk) {
+            if (t0 + tc >= t_end) continue;                            // uniform over the CTA
+            f32x2 h0[2][2], hh[kChunk][2][2], dAt[2][2] = {};
 #pragma unroll
-        for (int t = 0; t < kChunk; ++t) {
-            const float4 q = sp[t * CPB + ch];
-            float Bf[4];
-            get4(sB + t * NP + ln * 4, Bf);
-            const float ux = q.x * q.y;
+            for (int c = 0; c < 2; ++c) {
+                const bool on = c0 + c < cb.count;
+                order(on ? ck_h[c] : make_float4(0.f, 0.f, 0.f, 0.f), h0[c]);
+                if (seg > 0) {
+                    const float U = on ? ck_u[c] : 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) hh[t][i] = fmaf(exp2_fast(q.x * A2[i]), t ? hh[t - 1][i] : h0[i], ux * Bf[i]);
-        }
-#pragma unroll
-        for (int tb = kChunk - TB; tb >= 0; tb -= TB) {
-            float s1[TB], s2[TB];
-#pragma unroll
-            for (int k = TB - 1; k >= 0; --k) {
-                const int t = tb + k;
-                const float4 q = sp[t * CPB + ch];
-                float Bf[4], Cf[4], v[8];
-                get4(sB + t * NP + ln * 4, Bf);
-                get4(sC + t * NP + ln * 4, Cf);
-                const float ux = q.x * q.y;
-                s1[k] = s2[k] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float av = exp2_fast(q.x * A2[i]);
-                    dh[i] = fmaf(Cf[i], q.z, dh[i]);
-                    v[i] = dh[i] * ux;
-                    v[4 + i] = q.z * hh[t][i];
-                    s1[k] = fmaf(dh[i], Bf[i], s1[k]);
-                    dh[i] *= av;                                       // a dh: what reaches h_{t-1}
-                    const float r = dh[i] * (t ? hh[t > 0 ? t - 1 : 0][i] : h0[i]);
-                    s2[k] = fmaf(A2[i], r, s2[k]);
-                    dA[i] = fmaf(q.x, r, dA[i]);
+                    for (int p = 0; p < 2; ++p) h0[c][p] = fma2(exp2_2(mul2(pk(U, U), A2[c][p])), hin[c][p], h0[c][p]);
                 }
-                lane_reduce<8, CL, LN>(v, lane);
-                if (reduced_owner<8, CL, LN>(lane)) {
-                    constexpr int KEPT = 8 / CL > 1 ? 8 / CL : 1;
-                    const int first = reduced_first<8, CL, LN>(lane);
+            }
+            if (t0 + tc > t_begin) checkpoint(t0 + tc - kChunk);
 #pragma unroll
-                    for (int j = 0; j < KEPT; ++j) {
-                        const int idx = first + j;
-                        sr[(warp * kChunk + t) * 2 * NP + (idx >> 2) * NP + ln * 4 + (idx & 3)] = v[j];
+            for (int k = 0; k < kChunk; ++k) {
+                const int t = tc + k;
+                const float4 q = su[t * PAIRS + pr];
+                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(sB + (m * kTile + t) * NP + ln * 4);
+                const f32x2 Bp[2] = {Bv.x, Bv.y}, uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        hh[k][c][p] = fma2(exp2_2(mul2(uu[c], A2[c][p])), k ? hh[k ? k - 1 : 0][c][p] : h0[c][p], mul2(ux[c], Bp[p]));
+            }
+#pragma unroll
+            for (int kb = kChunk - TB; kb >= 0; kb -= TB) {
+                float s1[CNT], s2[CNT];
+#pragma unroll
+                for (int kk = TB - 1; kk >= 0; --kk) {
+                    const int k = kb + kk, t = tc + k;
+                    const float4 q = su[t * PAIRS + pr];
+                    const float2 gv = sg[t * PAIRS + pr];
+                    const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(sB + (m * kTile + t) * NP + ln * 4);
+                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2 *>(sC + (m * kTile + t) * NP + ln * 4);
+                    const f32x2 Bp[2] = {Bv.x, Bv.y}, Cp[2] = {Cv.x, Cv.y};
+                    const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
+                    const f32x2 gg[2] = {pk(gv.x, gv.x), pk(gv.y, gv.y)};
+                    f32x2 vB[2], vC[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        f32x2 a1, a2;
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const f32x2 av = exp2_2(mul2(uu[c], A2[c][p]));
+                            dh[c][p] = fma2(Cp[p], gg[c], dh[c][p]);
+                            vB[p] = c ? fma2(dh[c][p], ux[c], vB[p]) : mul2(dh[c][p], ux[c]);
+                            vC[p] = c ? fma2(gg[c], hh[k][c][p], vC[p]) : mul2(gg[c], hh[k][c][p]);
+                            a1 = p ? fma2(dh[c][p], Bp[p], a1) : mul2(dh[c][p], Bp[p]);
+                            dh[c][p] = mul2(dh[c][p], av);             // a dh: what reaches h_{t-1}
+                            const f32x2 r = mul2(dh[c][p], k ? hh[k ? k - 1 : 0][c][p] : h0[c][p]);
+                            a2 = p ? fma2(A2[c][p], r, a2) : mul2(A2[c][p], r);
+                            dAt[c][p] = fma2(uu[c], r, dAt[c][p]);
+                        }
+                        s1[2 * kk + c] = sum2(a1);
+                        s2[2 * kk + c] = sum2(a2);
+                    }
+                    // dB, dC over the warp's channels: states 0, 1 of the lane's order are kept, then
+                    // state 0, then one of dB and dC
+                    if constexpr (CL >= 2) {
+                        vB[0] = add2(vB[0], __shfl_xor_sync(0xffffffffu, vB[1], LN));
+                        vC[0] = add2(vC[0], __shfl_xor_sync(0xffffffffu, vC[1], LN));
+                    }
+                    float *to = sr + (warp * kTile + t) * 2 * NP + ln * 4;
+                    float bl, bh, cl0, ch;
+                    unpk(vB[0], bl, bh);
+                    unpk(vC[0], cl0, ch);
+                    if constexpr (CL >= 4) {
+                        bl += __shfl_xor_sync(0xffffffffu, bh, 2 * LN);
+                        cl0 += __shfl_xor_sync(0xffffffffu, ch, 2 * LN);
+                    }
+                    if constexpr (CL >= 8) {
+                        const bool wc = cl & 4;
+                        float r = (wc ? cl0 : bl) + __shfl_xor_sync(0xffffffffu, wc ? bl : cl0, 4 * LN);
+                        if constexpr (CL >= 16) r += __shfl_xor_sync(0xffffffffu, r, 8 * LN);
+                        if (CL < 16 || !(cl & 8)) to[(wc ? NP : 0) + m] = r;
+                    } else if constexpr (CL == 4) {
+                        to[m] = bl;
+                        to[NP + m] = cl0;
+                    } else if constexpr (CL == 2) {
+                        *reinterpret_cast<float2 *>(to + m) = make_float2(bl, bh);
+                        *reinterpret_cast<float2 *>(to + NP + m) = make_float2(cl0, ch);
+                    } else {
+                        *reinterpret_cast<ulonglong2 *>(to) = make_ulonglong2(vB[0], vB[1]);
+                        *reinterpret_cast<ulonglong2 *>(to + NP) = make_ulonglong2(vC[0], vC[1]);
+                    }
+                }
+                lane_reduce<CNT, LN, 1>(s1, lane);
+                lane_reduce<CNT, LN, 1>(s2, lane);
+                if (owner) {
+                    const int t = tc + kb + myk;
+                    const float u = reinterpret_cast<const float *>(su + t * PAIRS + pr)[myc];
+                    const float g = reinterpret_cast<const float *>(sg + t * PAIRS + pr)[myc];
+                    const float2 xs = sx[t * CPB + c0 + myc];
+                    const float dd = fmaf(s2[0], kLn2, xs.x * s1[0]) * xs.y;
+                    so[t * CPB + c0 + myc] = make_float2(fmaf(u, s1[0], Dsk * g), dd);
+                    if (t0 + t < n) {
+                        dbs += dd;
+                        dDs = fmaf(g, xs.x, dDs);
                     }
                 }
             }
-            lane_reduce<TB, LN, 1>(s1, lane);
-            lane_reduce<TB, LN, 1>(s2, lane);
-            if (reduced_owner<TB, LN, 1>(lane)) {
-                const int t = tb + reduced_first<TB, LN, 1>(lane);
-                const float4 q = sp[t * CPB + ch];
-                const float dd = fmaf(s2[0], kLn2, q.y * s1[0]) * q.w;
-                so[t * OS + ch] = make_float2(fmaf(q.x, s1[0], Dsk * q.z), dd);
-                dbs += dd;
-                dDs = fmaf(q.z, q.y, dDs);
-            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) dA[c][p] = add2(dA[c][p], dAt[c][p]);
         }
         __syncthreads();
         // rows of dx and ddelta, and the CTA's share of dB and dC
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = tid + i * kThreads, t = e / ROW, cc = e % ROW * VEC;
-            if (t >= kChunk || t0 + t >= t_stop || cc >= cb.count) continue;
+            const int t = St::tok(i), c = St::chan(i);
+            if (t >= kTile || t0 + t >= t_stop || c >= cb.count) continue;
             float fx[VEC], fd[VEC];
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
-                const float2 o = so[t * OS + cc + k];
+                const float2 o = so[t * CPB + c + k];
                 fx[k] = t0 + t < n ? o.x : 0.f;
                 fd[k] = t0 + t < n ? o.y : 0.f;
             }
-            const size_t at = ((size_t)b * a.T + t0 + t) * D + cb.first + cc;
-            Vec v;
+            const size_t at = ((size_t)b * a.T + t0 + t) * D + cb.first + c;
+            typename St::Vec v;
             v.set(fx);
             v.store((T *)a.dx + at);
             v.set(fd);
             v.store((T *)a.ddelta + at);
         }
-        for (int e = tid; e < kChunk * 2 * NP; e += kThreads) {
+        for (int e = tid; e < kTile * 2 * NP; e += kGradThreads) {
             const int t = e / (2 * NP), k = e % (2 * NP);
-            if (t0 + t >= n) continue;
+            if (t0 + t >= n || t0 + t >= t_stop) continue;
             float f = 0.f;
 #pragma unroll
-            for (int q = 0; q < kThreads / 32; ++q) f += sr[(q * kChunk + t) * 2 * NP + k];
+            for (int q = 0; q < kGradWarps; ++q) f += sr[(q * kTile + t) * 2 * NP + k];
             ws[w.dbc + ((((size_t)b * a.T + t0 + t) * a.G + cb.group) * w.nb + blk % w.nb) * 2 * NP + k] = f;
         }
     }
-    // padding after the sequence's end
-    for (int t0 = t_begin + chunks * kChunk; t0 < t_stop; ++t0) {
-        for (int c = tid; c < cb.count; c += kThreads) {
-            const size_t at = ((size_t)b * a.T + t0) * D + cb.first + c;
-            ((T *)a.dx)[at] = from_f<T>(0.f);
-            ((T *)a.ddelta)[at] = from_f<T>(0.f);
-        }
+    // whole tiles of padding
+    const int done = t_begin + tiles * kTile;
+    for (int64_t e = tid; e < (int64_t)max(t_stop - done, 0) * cb.count; e += kGradThreads) {
+        const size_t at = ((size_t)b * a.T + done + e / cb.count) * D + cb.first + e % cb.count;
+        ((T *)a.dx)[at] = from_f<T>(0.f);
+        ((T *)a.ddelta)[at] = from_f<T>(0.f);
     }
     // one row of partials per (sequence, segment): dA [D][N], dD [D], dbias [D]
-    float one[2] = {dDs, dbs};
-    lane_reduce<1, LN, 1>(one, lane);
-    lane_reduce<1, LN, 1>(one + 1, lane);
-    if (live) {
-        float *row = ws + w.par + ((size_t)b * S + seg) * D * (N + 2);
+    float tot[4] = {myc ? 0.f : dDs, myc ? dDs : 0.f, myc ? 0.f : dbs, myc ? dbs : 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (ln * 4 + i < N) {
-                row[(size_t)d * N + ln * 4 + i] = dA[i];
-                if (seg == 0 && a.dS0) a.dS0[bd * N + ln * 4 + i] = dh[i];
-            }
-        }
-        if (ln == 0) {
-            row[(size_t)D * N + d] = one[0];
-            row[(size_t)D * N + D + d] = one[1];
+    for (int i = 0; i < 4; ++i) lane_reduce<1, LN, 1>(tot + i, lane);
+    float *row = ws + w.par + ((size_t)b * S + seg) * D * (N + 2);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        scatter(row, cb.first + c0 + c, c, dA[c]);
+        if (seg == 0 && a.dS0) scatter(a.dS0, bd + c, c, dh[c]);
+        if (ln == 0 && c0 + c < cb.count) {
+            row[(size_t)D * N + cb.first + c0 + c] = tot[c];
+            row[(size_t)D * N + D + cb.first + c0 + c] = tot[2 + c];
         }
     }
 }
 
 // Launch 3: dB, dC of one (token, group, which, n): the sum over the group's channel blocks.
-template <typename T> __global__ void __launch_bounds__(kThreads) groups_kernel(SsmArgs a, BwdWs w, const float *ws, int NP) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, rows = (int64_t)a.B * a.T * a.G;
+template <typename T> __global__ void __launch_bounds__(kSumThreads) groups_kernel(SsmArgs a, BwdWs w, const float *ws, int NP) {
+    const int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x, rows = (int64_t)a.B * a.T * a.G;
     const int64_t row = i / (2 * NP);
     const int k = (int)(i % (2 * NP)), which = k / NP, nn = k % NP;
     if (row >= rows || nn >= a.N) return;
@@ -399,62 +412,50 @@ template <typename T> __global__ void __launch_bounds__(kThreads) groups_kernel(
     ((T *)(which ? a.dC : a.dB))[row * a.N + nn] = from_f<T>(f);
 }
 
-template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
-template <typename T, int LN, int SPL, bool WIDE> cudaError_t run_states(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
-    using G = Geo<T, LN, SPL, WIDE>;
-    const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, G::CPB));
-    const size_t base = (2 * kTile * G::CPB + kTile * G::NP) * sizeof(float);
-    const size_t more = (kTile * G::NP + kTile * G::CPB) * sizeof(float);
-    if (w.sp.S > 1) {
-        cudaError_t e = allow_smem(states_kernel<T, LN, SPL, WIDE, true>, base + more);
-        if (e != cudaSuccess) return e;
-        states_kernel<T, LN, SPL, WIDE, true><<<dim3(nblk, w.sp.S), kThreads, base + more, s>>>(a, w, (float *)a.ws);
-    } else {
-        cudaError_t e = allow_smem(states_kernel<T, LN, SPL, WIDE, false>, base);
-        if (e != cudaSuccess) return e;
-        states_kernel<T, LN, SPL, WIDE, false><<<dim3(nblk, 1), kThreads, base, s>>>(a, w, (float *)a.ws);
-    }
-    return cudaGetLastError();
-}
-
 template <typename T, int LN, bool WIDE> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
-    constexpr int CPB = kThreads / LN, NP = 4 * LN;
-    const size_t smem = (4 * kChunk * CPB + 2 * kChunk * (CPB + 32 / LN) + 2 * kChunk * NP + 8 * kChunk * 2 * NP) * sizeof(float);
+    constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
+    const size_t smem = Staging<T, kGradThreads, CPB, NP, 3, WIDE>::BYTES + kTile * (PAIRS * 4 + CPB * 4 + PAIRS * 2 + 2 * 4 * NP + kGradWarps * 2 * NP) * sizeof(float);
     const cudaError_t e = allow_smem(grads_kernel<T, LN, WIDE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
-    grads_kernel<T, LN, WIDE><<<dim3(nblk, w.sp.S), kThreads, smem, s>>>(a, w, (float *)a.ws);
+    grads_kernel<T, LN, WIDE><<<dim3(nblk, w.sp.S), kGradThreads, smem, s>>>(a, w, (float *)a.ws);
     return cudaGetLastError();
 }
+template <typename T, int LN> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
+    const bool wide = a.D / a.G % 4 == 0 && a.N % 4 == 0;
+    return wide ? run_grads<T, LN, true>(a, w, s) : run_grads<T, LN, false>(a, w, s);
+}
 
-template <typename T, int LN, int SPL, int LNB> cudaError_t run_bwd(const SsmArgs &a, cudaStream_t s, int *nlaunch) {
+template <typename T> cudaError_t run_bwd(const SsmArgs &a, cudaStream_t s, int *nlaunch) {
     const BwdWs w = bwd_ws(a.B, a.T, a.D, a.G, a.N);
-    constexpr int V = 16 / (int)sizeof(T);
-    const int per = a.D / a.G;
+    float *ws = (float *)a.ws;
     cudaError_t e = cudaSuccess;
     if (a.T > 0 && a.B > 0) {
-        e = per % V == 0 && a.N % V == 0 ? run_states<T, LN, SPL, true>(a, w, s) : run_states<T, LN, SPL, false>(a, w, s);
+        const ScanWs sw{nullptr, ws + w.E, ws + w.U, ws + w.R, ws + w.chk, ws + w.ucum};
+        e = w.sp.S > 1 ? run_scan<T, kSegCheckpoints>(a, w.sp, sw, s, nlaunch) : run_scan<T, kCheckpoints>(a, w.sp, sw, s, nlaunch);
         if (e != cudaSuccess) return e;
-        *nlaunch += 1;
     }
     if (a.B > 0) {
-        e = per % 4 == 0 ? run_grads<T, LNB, true>(a, w, s) : run_grads<T, LNB, false>(a, w, s);
+        switch (grad_lanes(a.N)) {
+            case 2: e = run_grads<T, 2>(a, w, s); break;
+            case 4: e = run_grads<T, 4>(a, w, s); break;
+            case 8: e = run_grads<T, 8>(a, w, s); break;
+            case 16: e = run_grads<T, 16>(a, w, s); break;
+            default: e = run_grads<T, 32>(a, w, s); break;
+        }
         if (e != cudaSuccess) return e;
         *nlaunch += 1;
     }
     if (a.T > 0 && a.B > 0) {
         const int NP = padded_states(a.N);
         const int64_t items = (int64_t)a.B * a.T * a.G * 2 * NP;
-        groups_kernel<T><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, w, (const float *)a.ws, NP);
+        groups_kernel<T><<<(unsigned)((items + kSumThreads - 1) / kSumThreads), kSumThreads, 0, s>>>(a, w, ws, NP);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         *nlaunch += 1;
     }
-    return launch_sum_rows((const float *)a.ws + w.par, w.rows, (int64_t)a.D * (a.N + 2), a.dA, (int64_t)a.D * a.N, a.dD, a.D,
-                           a.ddelta_bias, s, nlaunch);
+    return launch_sum_rows(ws + w.par, w.rows, (int64_t)a.D * (a.N + 2), a.dA, (int64_t)a.D * a.N, a.dD, a.D, a.ddelta_bias, s,
+                           nlaunch);
 }
 
 }  // namespace
@@ -462,11 +463,7 @@ template <typename T, int LN, int SPL, int LNB> cudaError_t run_bwd(const SsmArg
 size_t ssm_bwd_workspace(int B, int T, int D, int G, int N) { return bwd_ws(B, T, D, G, N).total * sizeof(float); }
 
 cudaError_t launch_ssm_bwd(const SsmArgs &a, int dtype, cudaStream_t s, int *nlaunch) {
-    if (a.N <= 8) return dtype == kBF16 ? run_bwd<__nv_bfloat16, 2, 4, 2>(a, s, nlaunch) : run_bwd<float, 2, 4, 2>(a, s, nlaunch);
-    if (a.N <= 16) return dtype == kBF16 ? run_bwd<__nv_bfloat16, 4, 4, 4>(a, s, nlaunch) : run_bwd<float, 4, 4, 4>(a, s, nlaunch);
-    if (a.N <= 32) return dtype == kBF16 ? run_bwd<__nv_bfloat16, 4, 8, 8>(a, s, nlaunch) : run_bwd<float, 4, 8, 8>(a, s, nlaunch);
-    if (a.N <= 64) return dtype == kBF16 ? run_bwd<__nv_bfloat16, 8, 8, 16>(a, s, nlaunch) : run_bwd<float, 8, 8, 16>(a, s, nlaunch);
-    return dtype == kBF16 ? run_bwd<__nv_bfloat16, 8, 16, 32>(a, s, nlaunch) : run_bwd<float, 8, 16, 32>(a, s, nlaunch);
+    return dtype == kBF16 ? run_bwd<__nv_bfloat16>(a, s, nlaunch) : run_bwd<float>(a, s, nlaunch);
 }
 
 }  // namespace qd

@@ -1,0 +1,478 @@
+// The selective scan's recurrence over a sequence, as one kernel in four modes: with outputs,
+// and, without them, the states that the segmented forward and the backward start from.
+//
+//   h_t[n] = exp(u_t A[n]) h_{t-1}[n] + u_t x_t B_t[n]  per channel,  y_t = sum_n C_t[n] h_t[n] + D x_t
+//
+// Each (token, channel, state) costs one exponential and six operations and no state leaves
+// the chip, so on-chip throughput bounds it: instruction issue first, then the shared-memory
+// pipe (operands into registers) and the exponentials.
+//
+// A thread holds 2 channels by 4 states in registers (arithmetic on packed pairs of states);
+// LN lanes share a channel pair (4 LN = N rounded up).  Per token it reads 4 B, 4 C and two
+// (u, u x): 48 bytes for 8 states.  One channel by 4 states reads 40 bytes for 4 and is bound by
+// the shared-memory pipe; 2 by 8 reads less per state but needs as many instructions and halves
+// the warps, which the recurrence needs to cover its latencies.
+// A CTA of four warps takes CPB = 256 / LN channels of one sequence and walks its tokens in tiles
+// of 16, staged in shared memory as fp32 (softplus once per token and channel) while the next
+// two tiles are on their way.  y goes back through shared memory, so rows are written as they
+// are read.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace qd {
+namespace ssm {
+
+constexpr int kScanThreads = 128;
+constexpr int kTile = 16;             // tokens staged at a time
+constexpr int kChunk = 8;             // tokens between the backward's checkpoints
+
+__host__ __device__ constexpr int padded_states(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128; }
+
+// Channel blocks never cross a group of channels that share B and C.
+__host__ __device__ inline int channel_blocks(int D, int G, int CPB) { return G * ((D / G + CPB - 1) / CPB); }
+
+struct ChannelBlock {
+    int group, first, count;          // its group, its first channel and how many it has
+    __device__ __forceinline__ ChannelBlock(const SsmArgs &a, int block, int CPB) {
+        const int per = a.D / a.G, nb = (per + CPB - 1) / CPB;
+        group = block / nb;
+        const int at = (block % nb) * CPB;
+        first = group * per + at;
+        count = min(CPB, per - at);
+    }
+};
+
+// Tokens cut into S segments of `len` (a multiple of the tile): one when `ctas` CTAs already
+// number `enough`, else about `want` CTAs in all, of at least `least` tokens.
+struct Split {
+    int S, len;
+};
+inline Split split_tokens(int64_t ctas, int T, int64_t enough, int64_t want, int least) {
+    Split s{1, T > 0 ? T : 1};
+    if (ctas <= 0 || ctas >= enough) return s;
+    int64_t S = want / ctas, most = T / least;
+    if (S > most) S = most;
+    if (S < 2) return s;
+    s.len = (int)(((T + S - 1) / S + kTile - 1) / kTile * kTile);
+    s.S = (T + s.len - 1) / s.len;
+    return s;
+}
+
+// More dynamic shared memory than a launch gets without asking.
+template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
+    return bytes <= 48 * 1024 ? cudaSuccess
+                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+__device__ __forceinline__ int seq_len(const int *lens, int b, int T) { return lens ? min(max(lens[b], 0), T) : T; }
+
+// u = softplus(delta + bias), or the sum, of VEC channels.
+template <int VEC> __device__ __forceinline__ void step_sizes(float (&u)[VEC], const float (&bias)[VEC], int softplus) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) u[k] += bias[k];
+    if (softplus) {
+        float e0, e1, none = 0.f;
+        if constexpr (VEC == 1) softplus2(u[0], none, e0, e1);
+        else
+#pragma unroll
+            for (int k = 0; k + 1 < VEC; k += 2) softplus2(u[k], u[k + 1], e0, e1);
+    }
+}
+
+// Asynchronous copy of BYTES to shared memory, or zeros where there is nothing to copy.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src, bool on) {
+    const unsigned to = (unsigned)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(BYTES), "r"(on ? BYTES : 0) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// A tile of tokens on its way from global to shared memory: NA token arrays and B and C.  The raw
+// tile arrives by asynchronous copies, two tiles ahead, in one of kStages buffers; every thread
+// then reads back what it copied itself (so its own wait is enough), converts it and stages it
+// for the CTA.  A thread moves PER accesses of VEC channels per array; B and C go four states at a
+// time.  What is beyond the sequence, the block's channels or N arrives as zero.  Odd shapes (not
+// WIDE) have no aligned accesses: they are read one by one when they are staged.
+constexpr int kStages = 3;
+
+template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct Staging {
+    static constexpr int VEC = WIDE ? 4 : 1;
+    static constexpr int ROW = CPB / VEC;                              // accesses a token
+    static constexpr int PER = (kTile * ROW + THREADS - 1) / THREADS;
+    static constexpr int GROW = NP / 4, GALL = 2 * kTile * GROW;       // accesses of B a token; of both in all
+    static constexpr int GPER = (GALL + THREADS - 1) / THREADS;
+    static constexpr bool FIXED = THREADS % ROW == 0;                  // a thread's channels are the same every time
+    static constexpr int STAGE = WIDE ? (NA * kTile * CPB + 2 * kTile * NP) : 0;   // elements of a raw tile
+    static constexpr size_t BYTES = (size_t)kStages * STAGE * sizeof(T);
+    using Vec = Pack<T, VEC>;
+
+    __device__ __forceinline__ static int tok(int i) { return (threadIdx.x + i * THREADS) / ROW; }
+    __device__ __forceinline__ static int chan(int i) { return (threadIdx.x + i * THREADS) % ROW * VEC; }
+
+    // The parameter p (or 0) of the channels of access i.
+    __device__ __forceinline__ static void param(const float *p, const ChannelBlock &cb, int i, float (&f)[VEC]) {
+        const int c = chan(i);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[k] = p && c + k < cb.count ? p[cb.first + c + k] : 0.f;
+    }
+    __device__ __forceinline__ static const T *groups(const SsmArgs &a, const ChannelBlock &cb, int b, int64_t t, int which) {
+        return (const T *)(which ? a.Cm : a.Bm) + (((size_t)b * a.T + t) * a.G + cb.group) * a.N;
+    }
+    // Whether the whole tile at t0 is real: no padding, no channels beyond the block's.
+    __device__ __forceinline__ static bool full(const ChannelBlock &cb, int t0, int n) { return t0 + kTile <= n && cb.count == CPB; }
+    // Starts the copies of the tile at t0 into buffer `buf` (one group of copies, possibly empty).
+    __device__ __forceinline__ static void issue(T *raw, int buf, const SsmArgs &a, const ChannelBlock &cb, int b, int t0, int end,
+                                                 int n, bool both, const void *const (&src)[NA]) {
+        if constexpr (WIDE) {
+            static_assert(FIXED);
+            T *to = raw + (size_t)buf * STAGE;
+            if (t0 < end) {
+                const bool all = full(cb, t0, n);
+                const size_t base = (size_t)b * a.T * a.D + cb.first + chan(0);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    if (tok(i) >= kTile) break;
+                    const bool on = all || (t0 + tok(i) < n && chan(0) < cb.count);
+                    const size_t at = on ? base + (size_t)(t0 + tok(i)) * a.D : 0;
+#pragma unroll
+                    for (int j = 0; j < NA; ++j)
+                        copy_async<4 * sizeof(T)>(to + j * kTile * CPB + (threadIdx.x + i * THREADS) * 4, (const T *)src[j] + at, on);
+                }
+#pragma unroll
+                for (int i = 0; i < GPER; ++i) {
+                    const int e = threadIdx.x + i * THREADS, which = e / (kTile * GROW), r = e % (kTile * GROW);
+                    const int t = r / GROW, k = r % GROW * 4;
+                    if (e >= (both ? GALL : GALL / 2)) break;
+                    const bool on = t0 + t < n && k < a.N;
+                    copy_async<4 * sizeof(T)>(to + NA * kTile * CPB + e * 4, groups(a, cb, b, on ? t0 + t : 0, which) + (on ? k : 0), on);
+                }
+            }
+            copies_issued();
+        }
+    }
+    // Access i of token array j of the tile at t0, in buffer `buf`.
+    __device__ __forceinline__ static void get(const T *raw, int buf, int j, int i, const SsmArgs &a, const ChannelBlock &cb, int b,
+                                               int t0, int n, const void *src, float (&f)[VEC]) {
+        const int t = tok(i), c = chan(i);
+        Vec v;
+        if constexpr (WIDE) {
+            v.load(raw + (size_t)buf * STAGE + j * kTile * CPB + (threadIdx.x + i * THREADS) * 4);
+        } else {
+            v.zero();
+            if (t0 + t < n && c < cb.count) v.load((const T *)src + ((size_t)b * a.T + t0 + t) * a.D + cb.first + c);
+        }
+        v.get(f);
+    }
+    // put(which, t, k, f): B (0) or C (1) of token t, states k .. k + 3
+    template <typename F>
+    __device__ __forceinline__ static void get_groups(const T *raw, int buf, const SsmArgs &a, const ChannelBlock &cb, int b, int t0,
+                                                      int n, bool both, F put) {
+#pragma unroll
+        for (int i = 0; i < GPER; ++i) {
+            const int e = threadIdx.x + i * THREADS, which = e / (kTile * GROW), r = e % (kTile * GROW);
+            const int t = r / GROW, k = r % GROW * 4;
+            if (e >= (both ? GALL : GALL / 2)) break;
+            float f[4];
+            if constexpr (WIDE) {
+                Pack<T, 4> v;
+                v.load(raw + (size_t)buf * STAGE + NA * kTile * CPB + e * 4);
+                v.get(f);
+            } else {
+                const T *p = groups(a, cb, b, t0 + t, which) + k;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = t0 + t < n && k + j < a.N ? to_f(p[j]) : 0.f;
+            }
+            put(which, t, k, f);
+        }
+    }
+};
+
+enum ScanMode {
+    kOutputs,           // y and the final state
+    kEnds,              // the end and the sum of u of every segment but the last (segmented forward)
+    kCheckpoints,       // the state entering every chunk (backward, one segment)
+    kSegCheckpoints     // the same from a zero state per segment, and what joins segments (backward)
+};
+
+// Workspace arrays of the modes; states are [.., B, D, NP].
+struct ScanWs {
+    float *start;       // [1]: S0 or zero.  Read back by the outputs, so that S_final may be S0
+    float *E, *U;       // [S]: a segment's end (from zero; segment 0 from S0) and its sum of u
+    float *R;           // [S]: sum_t (prod_{s<=t} a_s) C_t dy_t over a segment
+    float *chk, *ucum;  // [chunks]: the state entering a chunk, and u summed from the segment's start
+};
+
+// Row of the staged y: bank of a (token, channel pair) free of conflicts.
+__host__ __device__ constexpr int scan_row(int LN) { return 256 / LN + (LN < 4 ? 0 : LN < 32 ? 64 / LN : 4); }
+
+template <typename T, int LN, bool WIDE, int MODE>
+__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split sp, ScanWs w) {
+    constexpr int PAIRS = kScanThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
+    constexpr bool OUT = MODE == kOutputs, SEG = MODE == kSegCheckpoints, CHK = SEG || MODE == kCheckpoints;
+    constexpr bool BOTH = OUT || SEG;                                  // C is needed
+    constexpr int TB = LN < 16 ? LN / 2 : 8, CNT = 2 * TB;             // tokens and sums over n joined at once
+    constexpr int YS = scan_row(LN);
+    using St = Staging<T, kScanThreads, CPB, NP, SEG ? 3 : 2, WIDE>;
+    constexpr int VEC = St::VEC, PER = St::PER;
+    extern __shared__ float4 smem4[];
+    T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
+    float4 *su = smem4 + St::BYTES / 16;                               // [kTile][PAIRS] (u0, u1, u0 x0, u1 x1)
+    float *sB = reinterpret_cast<float *>(su + kTile * PAIRS);         // [kTile][NP]
+    float *sC = sB + kTile * NP;                                       // [kTile][NP]         BOTH
+    float *sy = sC + kTile * NP;                                       // [kTile][YS] y       OUT
+    float *sg = sy;                                                    // [kTile][CPB] dy     SEG
+
+    const int lane = threadIdx.x & 31, ln = threadIdx.x % LN, pr = threadIdx.x / LN, seg = blockIdx.y;
+    const int nblk = channel_blocks(a.D, a.G, CPB), b = blockIdx.x / nblk;
+    const ChannelBlock cb(a, blockIdx.x % nblk, CPB);
+    const int D = a.D, N = a.N, c0 = 2 * pr;
+    const int n = seq_len(a.lens, b, a.T);
+    const int t_begin = seg * sp.len, t_stop = min(t_begin + sp.len, a.T), t_end = min(t_stop, n);
+    const size_t bd = (size_t)b * D + cb.first + c0, all = (size_t)a.B * D;
+
+    f32x2 A2[2][2], h[2][2], P[2][2], R[2][2];                         // A log2(e); pairs of states
+    const bool from_S0 = a.S0 && seg == 0 && (MODE != kOutputs || sp.S == 1);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float av[2], hv[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int k = ln * 4 + 2 * p + j;
+                const bool on = c0 + c < cb.count && k < N;
+                av[j] = on ? a.A[(size_t)(cb.first + c0 + c) * N + k] * kLog2e : 0.f;
+                hv[j] = on && from_S0 ? a.S0[(bd + c) * N + k] : 0.f;
+            }
+            A2[c][p] = pk(av[0], av[1]);
+            h[c][p] = pk(hv[0], hv[1]);
+            if (SEG) {
+                P[c][p] = pk(1.f, 1.f);
+                R[c][p] = 0;
+            }
+        }
+    // four states of a channel as they lie in the workspace
+    auto put_state = [&](float *base, size_t row, int c, const f32x2(&v)[2]) {
+        if (c0 + c < cb.count) *reinterpret_cast<ulonglong2 *>(base + (row + c) * NP + ln * 4) = make_ulonglong2(v[0], v[1]);
+    };
+    if (MODE == kEnds && seg == 0) {
+        put_state(w.start, bd, 0, h[0]);
+        put_state(w.start, bd, 1, h[1]);
+    }
+    if (OUT && sp.S > 1) {                                             // fold the segments before this one
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (c0 + c >= cb.count) continue;
+            for (int s = seg > 0 ? 0 : -1; s < max(seg, 0); ++s) {
+                const float *src = s < 0 ? w.start : w.E + s * all * NP;
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(src + (bd + c) * NP + ln * 4);
+                const float U = s < 0 ? 0.f : w.U[s * all + bd + c];
+                const f32x2 UU = pk(U, U);
+                h[c][0] = fma2(exp2_2(mul2(UU, A2[c][0])), h[c][0], e.x);
+                h[c][1] = fma2(exp2_2(mul2(UU, A2[c][1])), h[c][1], e.y);
+            }
+        }
+    }
+
+    float bias[VEC], skip[VEC];
+    if (St::FIXED) {
+        St::param(a.delta_bias, cb, 0, bias);
+        if (OUT) St::param(a.Dskip, cb, 0, skip);
+    }
+    auto issue = [&](int t0, int buf) {
+        if constexpr (SEG) St::issue(raw, buf, a, cb, b, t0, t_end, n, BOTH, {a.x, a.delta, a.dy});
+        else St::issue(raw, buf, a, cb, b, t0, t_end, n, BOTH, {a.x, a.delta});
+    };
+    f32x2 U = 0;                                                       // of the two channels
+    issue(t_begin, 0);
+    issue(t_begin + kTile, 1);
+    int buf = 0;
+    for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf = buf + 1 < kStages ? buf + 1 : 0) {
+        issue(t0 + 2 * kTile, buf + 2 < kStages ? buf + 2 : buf + 2 - kStages);
+        if constexpr (WIDE) copies_done<2>();
+        const bool full = St::full(cb, t0, n);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = St::tok(i), c = St::chan(i);
+            if (t >= kTile) break;
+            float u[VEC], x[VEC];
+            if (!St::FIXED) St::param(a.delta_bias, cb, i, bias);
+            St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
+            St::get(raw, buf, 1, i, a, cb, b, t0, n, a.delta, u);
+            step_sizes<VEC>(u, bias, a.softplus);
+            if (!full && !(t0 + t < n && c < cb.count)) {              // of the padding nothing counts
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) u[k] = 0.f;
+            }
+            if constexpr (VEC == 4) {
+#pragma unroll
+                for (int k = 0; k < 4; k += 2)
+                    su[t * PAIRS + (c + k) / 2] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
+            } else {
+                float *to = reinterpret_cast<float *>(su + t * PAIRS + c / 2) + (c & 1);
+                to[0] = u[0];
+                to[2] = u[0] * x[0];
+            }
+            if constexpr (SEG) {
+                float g[VEC];
+                St::get(raw, buf, 2, i, a, cb, b, t0, n, a.dy, g);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) sg[t * CPB + c + k] = g[k];
+            }
+        }
+        St::get_groups(raw, buf, a, cb, b, t0, n, BOTH, [&](int which, int t, int k, const float (&f)[4]) {
+            *reinterpret_cast<float4 *>((which ? sC : sB) + t * NP + k) = make_float4(f[0], f[1], f[2], f[3]);
+        });
+        __syncthreads();
+#pragma unroll 1
+        for (int tc = 0; tc < kTile; tc += kChunk) {
+            if (CHK && t0 + tc < t_end) {
+                const size_t row = (size_t)((t0 + tc) / kChunk) * all + bd;
+                put_state(w.chk, row, 0, h[0]);
+                put_state(w.chk, row, 1, h[1]);
+                if (SEG && ln == 0) {
+                    float u0, u1;
+                    unpk(U, u0, u1);
+                    if (c0 < cb.count) w.ucum[row] = u0;
+                    if (c0 + 1 < cb.count) w.ucum[row + 1] = u1;
+                }
+            }
+            constexpr int UNROLL = TB >= 4 ? 1 : 4 / TB;
+#pragma unroll UNROLL
+            for (int tb = 0; tb < kChunk; tb += TB) {
+                float v[CNT];
+#pragma unroll
+                for (int k = 0; k < TB; ++k) {
+                    const int t = tc + tb + k;
+                    const float4 q = su[t * PAIRS + pr];
+                    const ulonglong2 Bq = *reinterpret_cast<const ulonglong2 *>(sB + t * NP + ln * 4);
+                    const ulonglong2 Cq = BOTH ? *reinterpret_cast<const ulonglong2 *>(sC + t * NP + ln * 4) : ulonglong2{};
+                    const f32x2 Bv[2] = {Bq.x, Bq.y}, Cv[2] = {Cq.x, Cq.y};
+                    if (MODE == kEnds || SEG) U = add2(U, pk(q.x, q.y));
+                    const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        f32x2 acc = 0;
+                        const float g = SEG ? sg[t * CPB + c0 + c] : 0.f;
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const f32x2 av = exp2_2(mul2(uu[c], A2[c][p]));
+                            h[c][p] = fma2(av, h[c][p], mul2(ux[c], Bv[p]));
+                            if (OUT) acc = p ? fma2(Cv[p], h[c][p], acc) : mul2(Cv[p], h[c][p]);
+                            if (SEG) {
+                                P[c][p] = mul2(P[c][p], av);
+                                R[c][p] = fma2(P[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
+                            }
+                        }
+                        if (OUT) v[2 * k + c] = sum2(acc);
+                    }
+                }
+                if (OUT) {
+                    lane_reduce<CNT, LN, 1>(v, lane);
+                    const int first = reduced_first<CNT, LN, 1>(lane);  // 2 k + c of v[0]
+                    if (reduced_owner<CNT, LN, 1>(lane)) sy[(tc + tb + first / 2) * YS + c0 + (first & 1)] = v[0];
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (OUT) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int t = St::tok(i), c = St::chan(i);
+                if (t >= kTile || t0 + t >= t_stop || c >= cb.count) continue;
+                if (!St::FIXED) St::param(a.Dskip, cb, i, skip);
+                float f[VEC], x[VEC];
+                St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
+                if constexpr (VEC == 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(sy + t * YS + c);
+                    f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+                } else {
+                    f[0] = sy[t * YS + c];
+                }
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    if (a.Dskip) f[k] = fmaf(skip[k], x[k], f[k]);
+                    if (!full && t0 + t >= n) f[k] = 0.f;
+                }
+                typename St::Vec o;
+                o.set(f);
+                o.store((T *)a.y + ((size_t)b * a.T + t0 + t) * D + cb.first + c);
+            }
+        }
+    }
+    if constexpr (OUT) {                                               // whole tiles of padding
+        const int done = t_begin < t_end ? t_begin + (t_end - t_begin + kTile - 1) / kTile * kTile : t_begin;
+        for (int64_t e = threadIdx.x; e < (int64_t)max(t_stop - done, 0) * cb.count; e += kScanThreads)
+            ((T *)a.y)[((size_t)b * a.T + done + e / cb.count) * D + cb.first + e % cb.count] = from_f<T>(0.f);
+    }
+    if (OUT && a.S_final && seg == sp.S - 1) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float v[2];
+                unpk(h[c][p], v[0], v[1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int k = ln * 4 + 2 * p + j;
+                    if (c0 + c < cb.count && k < N) a.S_final[(bd + c) * N + k] = v[j];
+                }
+            }
+    }
+    if (MODE == kEnds || SEG) {
+        const size_t row = seg * all + bd;
+        put_state(w.E, row, 0, h[0]);
+        put_state(w.E, row, 1, h[1]);
+        if (SEG) {
+            put_state(w.R, row, 0, R[0]);
+            put_state(w.R, row, 1, R[1]);
+        }
+        if (ln == 0) {
+            float u0, u1;
+            unpk(U, u0, u1);
+            if (c0 < cb.count) w.U[row] = u0;
+            if (c0 + 1 < cb.count) w.U[row + 1] = u1;
+        }
+    }
+}
+
+template <typename T, int LN, bool WIDE, int MODE>
+cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
+    constexpr int CPB = 2 * kScanThreads / LN, NP = 4 * LN, YS = scan_row(LN);
+    const size_t raw = Staging<T, kScanThreads, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, WIDE>::BYTES;
+    const size_t smem = raw + (kTile * 2 * CPB + 2 * kTile * NP + kTile * YS) * sizeof(float);
+    const cudaError_t e = allow_smem(scan_kernel<T, LN, WIDE, MODE>, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
+    scan_kernel<T, LN, WIDE, MODE><<<dim3(nblk, MODE == kEnds ? sp.S - 1 : sp.S), kScanThreads, smem, s>>>(a, sp, w);
+    const cudaError_t r = cudaGetLastError();
+    if (r == cudaSuccess) *nlaunch += 1;
+    return r;
+}
+
+// Whole groups of four along a group's channels and along the states go by vector accesses.
+template <typename T, int LN, int MODE>
+cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
+    const bool wide = a.D / a.G % 4 == 0 && a.N % 4 == 0;
+    return wide ? run_scan<T, LN, true, MODE>(a, sp, w, s, nlaunch) : run_scan<T, LN, false, MODE>(a, sp, w, s, nlaunch);
+}
+
+template <typename T, int MODE>
+cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
+    switch (padded_states(a.N)) {
+        case 8: return run_scan<T, 2, MODE>(a, sp, w, s, nlaunch);
+        case 16: return run_scan<T, 4, MODE>(a, sp, w, s, nlaunch);
+        case 32: return run_scan<T, 8, MODE>(a, sp, w, s, nlaunch);
+        case 64: return run_scan<T, 16, MODE>(a, sp, w, s, nlaunch);
+        default: return run_scan<T, 32, MODE>(a, sp, w, s, nlaunch);
+    }
+}
+
+// CTAs of the scan along sequences and channels.
+inline int64_t scan_ctas(int B, int D, int G, int N) {
+    return (int64_t)B * channel_blocks(D, G, 2 * kScanThreads * 4 / padded_states(N));
+}
+
+}  // namespace ssm
+}  // namespace qd

@@ -11,17 +11,54 @@ from __future__ import annotations
 
 import torch
 
-from . import (_call, _check, _dtype_code, _need, _ptr, _same_device, _stream, _workspace, load_library)
+from . import _check, _dtype_code, _need, _same_device, _stream, load_library
 
 F32, I32 = torch.float32, torch.int32
 
 
-def _new(t, shape, dtype, device, name):
+def _arg(t, name, dtype, shape, dev, optional=False):
+    """The address of an argument that is what it has to be; an error that says what is wrong
+    otherwise.  One token's call spends most of its time on the host, so the usual case is a
+    single test."""
+    if t is None and optional:
+        return None
+    if t is not None and t.device == dev and t.dtype == dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    _same_device(dev, t)
+
+
+def _new(t, name, dtype, shape, dev):
     """The caller's output after a check, or a fresh one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, dtype, shape)
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _arg(t, name, dtype, shape, dev)
     return t
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(nbytes, workspace, dev):
+    """Address and size of the caller's workspace, or of a fresh one of nbytes, and its owner."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _same_device(dev, workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _run(name, dev, stream, *args):
+    """Calls the entry point `name` with `dev` current and the stream as its last argument."""
+    fn = getattr(load_library(), name)
+    st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, st), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, st), name)
 
 
 def short_conv_fwd(x, w, bias=None, S0=None, *, lens=None, silu=True, y=None, S_final=None, return_final=True,
@@ -31,18 +68,13 @@ def short_conv_fwd(x, w, bias=None, S0=None, *, lens=None, silu=True, y=None, S_
     the call, or None (= 0).  Returns (y, S_final), S_final the last W - 1 inputs."""
     B, T, D = x.shape
     W, dt, dev = w.shape[-1], x.dtype, x.device
-    _need(x, "x", dt, (B, T, D))
-    _need(w, "w", F32, (D, W))
-    _need(bias, "bias", F32, (D,), optional=True)
-    _need(S0, "S0", dt, (B, W - 1, D), optional=True)
-    _need(lens, "lens", I32, (B,), optional=True)
+    args = (_arg(x, "x", dt, (B, T, D), dev), _arg(w, "w", F32, (D, W), dev), _arg(bias, "bias", F32, (D,), dev, True),
+            _arg(S0, "S0", dt, (B, W - 1, D), dev, True), _arg(lens, "lens", I32, (B,), dev, True))
     code = _dtype_code(x)
-    y = _new(y, (B, T, D), dt, dev, "y")
+    y = _new(y, "y", dt, (B, T, D), dev)
     if S_final is not None or return_final:
-        S_final = _new(S_final, (B, W - 1, D), dt, dev, "S_final")
-    _same_device(dev, w, bias, S0, lens, y, S_final)
-    _check(_call(dev, load_library().short_conv_fwd, _ptr(x), _ptr(w), _ptr(bias), _ptr(S0), _ptr(lens), _ptr(y),
-                 _ptr(S_final), B, T, D, W, int(silu), code, _stream(stream, dev)), "short_conv_fwd")
+        S_final = _new(S_final, "S_final", dt, (B, W - 1, D), dev)
+    _run("short_conv_fwd", dev, stream, *args, y.data_ptr(), _adr(S_final), B, T, D, W, int(silu), code)
     return y, S_final
 
 
@@ -51,15 +83,11 @@ def short_conv_step(S, x, w, bias=None, *, silu=True, y=None, stream=None):
     inputs, updated in place.  Returns y [N,D]."""
     N, D = x.shape
     W, dt, dev = w.shape[-1], x.dtype, x.device
-    _need(x, "x", dt, (N, D))
-    _need(S, "S", dt, (N, W - 1, D))
-    _need(w, "w", F32, (D, W))
-    _need(bias, "bias", F32, (D,), optional=True)
+    args = (_arg(S, "S", dt, (N, W - 1, D), dev), _arg(x, "x", dt, (N, D), dev), _arg(w, "w", F32, (D, W), dev),
+            _arg(bias, "bias", F32, (D,), dev, True))
     code = _dtype_code(x)
-    y = _new(y, (N, D), dt, dev, "y")
-    _same_device(dev, S, w, bias, y)
-    _check(_call(dev, load_library().short_conv_step, _ptr(S), _ptr(x), _ptr(w), _ptr(bias), _ptr(y), N, D, W,
-                 int(silu), code, _stream(stream, dev)), "short_conv_step")
+    y = _new(y, "y", dt, (N, D), dev)
+    _run("short_conv_step", dev, stream, *args, y.data_ptr(), N, D, W, int(silu), code)
     return y
 
 
@@ -73,37 +101,26 @@ def short_conv_bwd(x, w, bias, S0, dy, dS_final=None, *, lens=None, silu=True, w
     Returns a dict dx, dw, dbias (None without a bias), dS0 (None unless want_dS0)."""
     B, T, D = x.shape
     W, dt, dev = w.shape[-1], x.dtype, x.device
-    _need(x, "x", dt, (B, T, D))
-    _need(w, "w", F32, (D, W))
-    _need(bias, "bias", F32, (D,), optional=True)
-    _need(S0, "S0", dt, (B, W - 1, D), optional=True)
-    _need(lens, "lens", I32, (B,), optional=True)
-    _need(dy, "dy", dt, (B, T, D))
-    _need(dS_final, "dS_final", dt, (B, W - 1, D), optional=True)
+    args = (_arg(x, "x", dt, (B, T, D), dev), _arg(w, "w", F32, (D, W), dev), _arg(bias, "bias", F32, (D,), dev, True),
+            _arg(S0, "S0", dt, (B, W - 1, D), dev, True), _arg(lens, "lens", I32, (B,), dev, True),
+            _arg(dy, "dy", dt, (B, T, D), dev), _arg(dS_final, "dS_final", dt, (B, W - 1, D), dev, True))
     code = _dtype_code(x)
     g = {"dx": torch.empty_like(x), "dw": torch.empty_like(w),
          "dbias": None if bias is None else torch.empty_like(bias),
          "dS0": torch.empty((B, W - 1, D), dtype=dt, device=dev) if want_dS0 else None}
-    workspace, wsb = _workspace(short_conv_bwd_workspace_bytes(B, T, D, W, code), workspace, dev)
-    _same_device(dev, w, bias, S0, lens, dy, dS_final, workspace)
-    _check(_call(dev, load_library().short_conv_bwd, _ptr(x), _ptr(w), _ptr(bias), _ptr(S0), _ptr(lens), _ptr(dy),
-                 _ptr(dS_final), _ptr(g["dx"]), _ptr(g["dw"]), _ptr(g["dbias"]), _ptr(g["dS0"]), B, T, D, W,
-                 int(silu), code, _ptr(workspace), wsb, _stream(stream, dev)), "short_conv_bwd")
+    ws, wsb, hold = _scratch(short_conv_bwd_workspace_bytes(B, T, D, W, code), workspace, dev)
+    _run("short_conv_bwd", dev, stream, *args, *map(_adr, g.values()), B, T, D, W, int(silu), code, ws, wsb)
     return g
 
 
 def _ssm_inputs(x, delta, A, B, C, D, delta_bias):
     """Checks what every form of the scan takes; tokens are x's leading dimensions."""
-    tok, ch, dt = tuple(x.shape[:-1]), x.shape[-1], x.dtype
+    tok, ch, dt, dev = tuple(x.shape[:-1]), x.shape[-1], x.dtype, x.device
     N, G = A.shape[-1], B.shape[-2]
-    _need(x, "x", dt, (*tok, ch))
-    _need(delta, "delta", dt, (*tok, ch))
-    _need(A, "A", F32, (ch, N))
-    _need(B, "B", dt, (*tok, G, N))
-    _need(C, "C", dt, (*tok, G, N))
-    _need(D, "D", F32, (ch,), optional=True)
-    _need(delta_bias, "delta_bias", F32, (ch,), optional=True)
-    return ch, G, N, _dtype_code(x)
+    args = (_arg(x, "x", dt, (*tok, ch), dev), _arg(delta, "delta", dt, (*tok, ch), dev), _arg(A, "A", F32, (ch, N), dev),
+            _arg(B, "B", dt, (*tok, G, N), dev), _arg(C, "C", dt, (*tok, G, N), dev),
+            _arg(D, "D", F32, (ch,), dev, True), _arg(delta_bias, "delta_bias", F32, (ch,), dev, True))
+    return args, ch, G, N, _dtype_code(x), dev
 
 
 def ssm_workspace_bytes(B, T, D, G, N, dtype) -> int:
@@ -117,34 +134,24 @@ def ssm_fwd(x, delta, A, B, C, D=None, delta_bias=None, S0=None, *, lens=None, s
     None; S0 [B,D,N] or None.  The step size is softplus(delta + delta_bias), or the sum itself
     with softplus=False.  Returns (y, S_final)."""
     nb, T, _ = x.shape
-    ch, G, N, code = _ssm_inputs(x, delta, A, B, C, D, delta_bias)
-    dev = x.device
-    _need(S0, "S0", F32, (nb, ch, N), optional=True)
-    _need(lens, "lens", I32, (nb,), optional=True)
-    y = _new(y, (nb, T, ch), x.dtype, dev, "y")
+    args, ch, G, N, code, dev = _ssm_inputs(x, delta, A, B, C, D, delta_bias)
+    args += (_arg(S0, "S0", F32, (nb, ch, N), dev, True), _arg(lens, "lens", I32, (nb,), dev, True))
+    y = _new(y, "y", x.dtype, (nb, T, ch), dev)
     if S_final is not None or return_final:
-        S_final = _new(S_final, (nb, ch, N), F32, dev, "S_final")
-    workspace, wsb = _workspace(ssm_workspace_bytes(nb, T, ch, G, N, code), workspace, dev)
-    _same_device(dev, delta, A, B, C, D, delta_bias, S0, lens, y, S_final, workspace)
-    _check(_call(dev, load_library().ssm_fwd, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                 _ptr(delta_bias), _ptr(S0), _ptr(lens), _ptr(y), _ptr(S_final), nb, T, ch, G, N, int(softplus), code,
-                 _ptr(workspace), wsb, _stream(stream, dev)), "ssm_fwd")
+        S_final = _new(S_final, "S_final", F32, (nb, ch, N), dev)
+    ws, wsb, hold = _scratch(ssm_workspace_bytes(nb, T, ch, G, N, code), workspace, dev)
+    _run("ssm_fwd", dev, stream, *args, y.data_ptr(), _adr(S_final), nb, T, ch, G, N, int(softplus), code, ws, wsb)
     return y, S_final
 
 
 def ssm_step(S, x, delta, A, B, C, D=None, delta_bias=None, *, softplus=True, y=None, stream=None):
     """One token of the scan: x, delta [N,D]; B, C [N,G,states]; S [N,D,states] float32 updated in
     place; the rest as in ssm_fwd.  Returns y [N,D]."""
-    nb = x.shape[0]
-    if x.dim() != 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [N, D]")
-    ch, G, N, code = _ssm_inputs(x, delta, A, B, C, D, delta_bias)
-    dev = x.device
-    _need(S, "S", F32, (nb, ch, N))
-    y = _new(y, (nb, ch), x.dtype, dev, "y")
-    _same_device(dev, S, delta, A, B, C, D, delta_bias, y)
-    _check(_call(dev, load_library().ssm_step, _ptr(S), _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                 _ptr(delta_bias), _ptr(y), nb, ch, G, N, int(softplus), code, _stream(stream, dev)), "ssm_step")
+    nb, _ = x.shape
+    args, ch, G, N, code, dev = _ssm_inputs(x, delta, A, B, C, D, delta_bias)
+    S = _arg(S, "S", F32, (nb, ch, N), dev)
+    y = _new(y, "y", x.dtype, (nb, ch), dev)
+    _run("ssm_step", dev, stream, S, *args, y.data_ptr(), nb, ch, G, N, int(softplus), code)
     return y
 
 
@@ -158,49 +165,36 @@ def ssm_bwd(x, delta, A, B, C, D, delta_bias, S0, dy, dS_final=None, *, lens=Non
     dx, ddelta, dA, dB, dC, dD and ddelta_bias (None without the parameter), dS0 (None unless
     want_dS0)."""
     nb, T, _ = x.shape
-    ch, G, N, code = _ssm_inputs(x, delta, A, B, C, D, delta_bias)
-    dev = x.device
-    _need(S0, "S0", F32, (nb, ch, N), optional=True)
-    _need(lens, "lens", I32, (nb,), optional=True)
-    _need(dy, "dy", x.dtype, (nb, T, ch))
-    _need(dS_final, "dS_final", F32, (nb, ch, N), optional=True)
+    args, ch, G, N, code, dev = _ssm_inputs(x, delta, A, B, C, D, delta_bias)
+    args += (_arg(S0, "S0", F32, (nb, ch, N), dev, True), _arg(lens, "lens", I32, (nb,), dev, True),
+             _arg(dy, "dy", x.dtype, (nb, T, ch), dev), _arg(dS_final, "dS_final", F32, (nb, ch, N), dev, True))
     g = {"dx": torch.empty_like(x), "ddelta": torch.empty_like(x), "dA": torch.empty_like(A),
          "dB": torch.empty_like(B), "dC": torch.empty_like(C), "dD": None if D is None else torch.empty_like(D),
          "ddelta_bias": None if delta_bias is None else torch.empty_like(delta_bias),
          "dS0": torch.empty((nb, ch, N), dtype=F32, device=dev) if want_dS0 else None}
-    workspace, wsb = _workspace(ssm_bwd_workspace_bytes(nb, T, ch, G, N, code), workspace, dev)
-    _same_device(dev, delta, A, B, C, D, delta_bias, S0, lens, dy, dS_final, workspace)
-    _check(_call(dev, load_library().ssm_bwd, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                 _ptr(delta_bias), _ptr(S0), _ptr(lens), _ptr(dy), _ptr(dS_final), _ptr(g["dx"]), _ptr(g["ddelta"]),
-                 _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["ddelta_bias"]), _ptr(g["dS0"]),
-                 nb, T, ch, G, N, int(softplus), code, _ptr(workspace), wsb, _stream(stream, dev)), "ssm_bwd")
+    ws, wsb, hold = _scratch(ssm_bwd_workspace_bytes(nb, T, ch, G, N, code), workspace, dev)
+    _run("ssm_bwd", dev, stream, *args, *map(_adr, g.values()), nb, T, ch, G, N, int(softplus), code, ws, wsb)
     return g
 
 
 def _norm_inputs(x, w, b, z):
     if x.dim() < 2:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [..., H, d]")
-    H, d = x.shape[-2:]
-    M = 1
+    dev, (H, d), M = x.device, x.shape[-2:], 1
     for n in x.shape[:-2]:
         M *= n
-    _need(x, "x", x.dtype, x.shape)
-    _need(w, "w", F32, (H, d), optional=True)
-    _need(b, "b", F32, (H, d), optional=True)
-    _need(z, "z", x.dtype, x.shape, optional=True)
-    return M, H, d, _dtype_code(x)
+    args = (_arg(x, "x", x.dtype, x.shape, dev), _arg(w, "w", F32, (H, d), dev, True),
+            _arg(b, "b", F32, (H, d), dev, True), _arg(z, "z", x.dtype, x.shape, dev, True))
+    return args, M, H, d, _dtype_code(x), dev
 
 
 def group_norm_fwd(x, w=None, b=None, z=None, *, eps=1e-5, center=True, silu=True, y=None, stream=None):
     """Group norm of each token's channels: x [..., H, d], H groups of d channels; w, b [H,d] or
     None (1, 0).  center=False: the root mean square in place of the mean and variance.  With a
     gate z (x's shape) y = n SiLU(z), else y = SiLU(n); silu=False: the identity in its place."""
-    M, H, d, code = _norm_inputs(x, w, b, z)
-    dev = x.device
-    y = _new(y, tuple(x.shape), x.dtype, dev, "y")
-    _same_device(dev, w, b, z, y)
-    _check(_call(dev, load_library().group_norm_fwd, _ptr(x), _ptr(w), _ptr(b), _ptr(z), _ptr(y), M, H, d, eps,
-                 int(center), int(silu), code, _stream(stream, dev)), "group_norm_fwd")
+    args, M, H, d, code, dev = _norm_inputs(x, w, b, z)
+    y = _new(y, "y", x.dtype, x.shape, dev)
+    _run("group_norm_fwd", dev, stream, *args, y.data_ptr(), M, H, d, eps, int(center), int(silu), code)
     return y
 
 
@@ -211,15 +205,12 @@ def group_norm_bwd_workspace_bytes(M, H, d, dtype) -> int:
 def group_norm_bwd(x, w, b, z, dy, *, eps=1e-5, center=True, silu=True, workspace=None, stream=None):
     """Backward of group_norm_fwd: gradients of sum(dy * y).  Returns a dict dx, dz, dw, db (None
     without the input)."""
-    M, H, d, code = _norm_inputs(x, w, b, z)
-    dev = x.device
-    _need(dy, "dy", x.dtype, x.shape)
+    args, M, H, d, code, dev = _norm_inputs(x, w, b, z)
+    dy = _arg(dy, "dy", x.dtype, x.shape, dev)
     g = {"dx": torch.empty_like(x), "dz": None if z is None else torch.empty_like(z),
          "dw": None if w is None else torch.empty_like(w), "db": None if b is None else torch.empty_like(b)}
-    workspace, wsb = _workspace(group_norm_bwd_workspace_bytes(M, H, d, code) if w is not None or b is not None else 0,
-                                workspace, dev)
-    _same_device(dev, w, b, z, dy, workspace)
-    _check(_call(dev, load_library().group_norm_bwd, _ptr(x), _ptr(w), _ptr(b), _ptr(z), _ptr(dy), _ptr(g["dx"]),
-                 _ptr(g["dz"]), _ptr(g["dw"]), _ptr(g["db"]), M, H, d, eps, int(center), int(silu), code,
-                 _ptr(workspace), wsb, _stream(stream, dev)), "group_norm_bwd")
+    need = 0 if w is None and b is None else group_norm_bwd_workspace_bytes(M, H, d, code)
+    ws, wsb, hold = _scratch(need, workspace, dev)
+    _run("group_norm_bwd", dev, stream, *args, dy, *map(_adr, g.values()), M, H, d, eps, int(center), int(silu), code,
+         ws, wsb)
     return g
