@@ -22,63 +22,33 @@ struct NormPlan {
     int lpg, HB, MB, nhb, gm;
 };
 
-__device__ __forceinline__ float group_total(float v, int lpg, float *sm) {
-    if (lpg <= 32) {
-        for (int o = lpg / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-    }
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();                                   // the last total has been read by all
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.f;
+template <int CNT> __device__ __forceinline__ void group_totals(float (&v)[CNT], int lpg, float *sm) {
+    auto join = [&](int o) {
 #pragma unroll
-    for (int i = 0; i < kNormThreads / 32; ++i) t += sm[i];
-    return t;
-}
-
-template <int VEC> __device__ __forceinline__ void load_param(const float *p, float (&f)[VEC]) {
-    if constexpr (VEC >= 4) {
+        for (int i = 0; i < CNT; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    };
+    if (lpg > 16) join(16);
+    if (lpg > 8) join(8);
+    if (lpg > 4) join(4);
+    if (lpg > 2) join(2);
+    if (lpg > 1) join(1);
+    if (lpg > 32) {
+        __syncthreads();                               // the last totals have been read by all
+        if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-            const float4 v = reinterpret_cast<const float4 *>(p)[i];
-            f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+            for (int i = 0; i < CNT; ++i) sm[(threadIdx.x >> 5) * CNT + i] = v[i];
         }
-    } else {
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] = p[i];
+        for (int i = 0; i < CNT; ++i) {
+            v[i] = 0.f;
+#pragma unroll
+            for (int q = 0; q < kNormThreads / 32; ++q) v[i] += sm[q * CNT + i];
+        }
     }
 }
 
-// xh of the thread's channels of one group, and the group's rstd.
-template <int VEC, int K>
-__device__ __forceinline__ float normalise(float (&v)[K][VEC], const bool (&on)[K], int d, int center, float eps, int lpg,
-                                           float *sm) {
-    const float inv_d = 1.f / (float)d;
-    if (center) {
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) s += v[k][c];
-        const float mean = group_total(s, lpg, sm) * inv_d;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) v[k][c] = on[k] ? v[k][c] - mean : 0.f;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) q = fmaf(v[k][c], v[k][c], q);
-    const float rstd = 1.f / sqrtf(group_total(q, lpg, sm) * inv_d + eps);
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) v[k][c] *= rstd;
-    return rstd;
-}
+__device__ __forceinline__ f32x2 both(float c) { return pk(c, c); }
 
 // The thread's place: group h (or none), first token, and its K channel offsets.
 template <int VEC, int K> struct Place {
@@ -97,27 +67,70 @@ template <int VEC, int K> struct Place {
             on[k] = live && c[k] < a.d;
         }
     }
+    // the group's parameter, or `none` where there is none
+    __device__ __forceinline__ void param(const float *p, int d, float none, f32x2 (&f)[K][(VEC + 1) / 2]) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            Pack<float, VEC < 4 ? VEC : 4> q[VEC < 4 ? 1 : VEC / 4];
+#pragma unroll
+            for (int i = 0; i < (VEC + 1) / 2; ++i) f[k][i] = both(none);
+            if (p && on[k]) {
+#pragma unroll
+                for (int i = 0; i < (VEC < 4 ? 1 : VEC / 4); ++i) {
+                    q[i].load(p + (size_t)h * d + c[k] + 4 * i);
+                    f32x2 g[VEC < 4 ? 1 : 2];
+                    q[i].get2(g);
+#pragma unroll
+                    for (int j = 0; j < (VEC < 4 ? 1 : 2); ++j) f[k][2 * i + j] = g[j];
+                }
+            }
+        }
+    }
 };
+
+// xh of the thread's channels of one group, and the group's rstd.
+template <int VEC, int K, int HV>
+__device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K], const NormArgs &a, float inv_d, int lpg, float *sm) {
+    if (a.center) {
+        f32x2 s = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < HV; ++i) s = add2(s, v[k][i]);
+        float tot[1] = {sum2(s)};
+        group_totals(tot, lpg, sm);
+        const float m = -tot[0] * inv_d;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < HV; ++i) v[k][i] = on[k] ? add2(v[k][i], pk(m, VEC == 1 ? 0.f : m)) : 0;
+    }
+    f32x2 q = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < HV; ++i) q = fma2(v[k][i], v[k][i], q);
+    float tot[1] = {sum2(q)};
+    group_totals(tot, lpg, sm);
+    const float rstd = 1.f / sqrtf(fmaf(tot[0], inv_d, a.eps));
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < HV; ++i) v[k][i] = mul2(v[k][i], both(rstd));
+    return rstd;
+}
 
 template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, NormPlan p) {
+    constexpr int HV = (VEC + 1) / 2;
     __shared__ float sm[kNormThreads / 32];
     const Place<VEC, K> at(a, p);
-    float w[K][VEC], b[K][VEC];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            w[k][c] = 1.f;
-            b[k][c] = 0.f;
-        }
-        if (at.on[k]) {
-            if (a.w) load_param<VEC>(a.w + (size_t)at.h * a.d + at.c[k], w[k]);
-            if (a.b) load_param<VEC>(a.b + (size_t)at.h * a.d + at.c[k], b[k]);
-        }
-    }
+    f32x2 w[K][HV], b[K][HV];
+    at.param(a.w, a.d, 1.f, w);
+    at.param(a.b, a.d, 0.f, b);
+    const float inv_d = 1.f / (float)a.d;
     const int64_t first = (int64_t)(blockIdx.x / p.nhb) * p.MB, turn = (int64_t)p.gm * p.MB;
-    Pack<T, VEC> x[K], z[K], xn[K], zn[K];
+    Pack<T, VEC> xn[K], zn[K];
     auto fetch = [&](int64_t m) {
         const size_t row = ((size_t)m * a.H + at.h) * a.d;
 #pragma unroll
@@ -135,29 +148,33 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
     for (int64_t m0 = first; m0 < a.M; m0 += turn) {
         const int64_t m = m0 + at.ml;
         const size_t row = ((size_t)m * a.H + at.h) * a.d;
-        float v[K][VEC];
+        f32x2 v[K][HV], t[K][HV];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            x[k] = xn[k];
-            z[k] = zn[k];
-            x[k].get(v[k]);
+            xn[k].get2(v[k]);
+            zn[k].get2(t[k]);
         }
         fetch(m + turn);                               // the next token's, while this one is computed
-        normalise<VEC, K>(v, at.on, a.d, a.center, a.eps, p.lpg, sm);
+        normalise<VEC, K, HV>(v, at.on, a, inv_d, p.lpg, sm);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float g[VEC];
-            z[k].get(g);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float n = fmaf(v[k][c], w[k][c], b[k][c]);
-                const float t = a.z ? g[c] : n;
-                const float act = a.silu ? t * sigmoid_f(t) : t;
-                v[k][c] = a.z ? n * act : act;
+            for (int i = 0; i < HV; ++i) v[k][i] = fma2(v[k][i], w[k][i], b[k][i]);
+            if (a.z) {
+                if (a.silu) {
+#pragma unroll
+                    for (int i = 0; i < HV; ++i) t[k][i] = mul2(t[k][i], sigmoid2(t[k][i]));
+                }
+#pragma unroll
+                for (int i = 0; i < HV; ++i) v[k][i] = mul2(v[k][i], t[k][i]);
+            } else if (a.silu) {
+#pragma unroll
+                for (int i = 0; i < HV; ++i) v[k][i] = mul2(v[k][i], sigmoid2(v[k][i]));
             }
             if (at.on[k] && m < a.M) {
-                x[k].set(v[k]);
-                x[k].store((T *)a.y + row + at.c[k]);
+                Pack<T, VEC> y;
+                y.set2(v[k]);
+                y.store((T *)a.y + row + at.c[k]);
             }
         }
     }
@@ -165,25 +182,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
 
 template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, NormPlan p) {
-    __shared__ float sm[kNormThreads / 32];
+    constexpr int HV = (VEC + 1) / 2;
+    __shared__ float sm[2 * kNormThreads / 32];
     extern __shared__ float sp[];
     const Place<VEC, K> at(a, p);
-    float w[K][VEC], b[K][VEC], dw[K][VEC], db[K][VEC];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            w[k][c] = 1.f;
-            b[k][c] = dw[k][c] = db[k][c] = 0.f;
-        }
-        if (at.on[k]) {
-            if (a.w) load_param<VEC>(a.w + (size_t)at.h * a.d + at.c[k], w[k]);
-            if (a.b) load_param<VEC>(a.b + (size_t)at.h * a.d + at.c[k], b[k]);
-        }
-    }
+    f32x2 w[K][HV], b[K][HV], dw[K][HV] = {}, db[K][HV] = {};
+    at.param(a.w, a.d, 1.f, w);
+    at.param(a.b, a.d, 0.f, b);
     const float inv_d = 1.f / (float)a.d;
     const int64_t begin = (int64_t)(blockIdx.x / p.nhb) * p.MB, turn = (int64_t)p.gm * p.MB;
-    Pack<T, VEC> x[K], z[K], dy[K], xn[K], zn[K], dyn[K];
+    Pack<T, VEC> xn[K], zn[K], dyn[K];
     auto fetch = [&](int64_t m) {
         const size_t row = ((size_t)m * a.H + at.h) * a.d;
 #pragma unroll
@@ -202,55 +210,63 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
     for (int64_t m0 = begin; m0 < a.M; m0 += turn) {
         const int64_t m = m0 + at.ml;
         const size_t row = ((size_t)m * a.H + at.h) * a.d;
-        float v[K][VEC];
+        f32x2 v[K][HV], g[K][HV], z[K][HV];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            x[k] = xn[k];
-            z[k] = zn[k];
-            dy[k] = dyn[k];
-            x[k].get(v[k]);
+            xn[k].get2(v[k]);
+            dyn[k].get2(g[k]);
+            zn[k].get2(z[k]);
         }
         fetch(m + turn);
-        const float rstd = normalise<VEC, K>(v, at.on, a.d, a.center, a.eps, p.lpg, sm);
-        float s1 = 0.f, s2 = 0.f, g[K][VEC];
+        const float rstd = normalise<VEC, K, HV>(v, at.on, a, inv_d, p.lpg, sm);
+        f32x2 s1 = 0, s2 = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float gate[VEC], dz[VEC];
-            dy[k].get(g[k]);
-            z[k].get(gate);
+            if (a.z) {
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float n = fmaf(v[k][c], w[k][c], b[k][c]);
-                const float t = a.z ? gate[c] : n;
-                const float s = a.silu ? sigmoid_f(t) : 1.f;
-                const float slope = a.silu ? silu_grad(t, s) : 1.f;
-                float dn;
-                if (a.z) {
-                    dz[c] = g[k][c] * n * slope;
-                    dn = g[k][c] * (a.silu ? t * s : t);
-                } else {
-                    dn = g[k][c] * slope;
+                for (int i = 0; i < HV; ++i) {
+                    const f32x2 n = fma2(v[k][i], w[k][i], b[k][i]), gn = mul2(g[k][i], n);
+                    if (a.silu) {
+                        const f32x2 s = sigmoid2(z[k][i]);
+                        g[k][i] = mul2(g[k][i], mul2(z[k][i], s));
+                        z[k][i] = mul2(gn, silu_grad2(z[k][i], s));
+                    } else {
+                        g[k][i] = mul2(g[k][i], z[k][i]);
+                        z[k][i] = gn;
+                    }
                 }
-                dw[k][c] = fmaf(dn, v[k][c], dw[k][c]);
-                db[k][c] += dn;
-                g[k][c] = dn * w[k][c];
-                s1 += g[k][c];
-                s2 = fmaf(g[k][c], v[k][c], s2);
+                if (at.on[k] && m < a.M) {
+                    Pack<T, VEC> o;
+                    o.set2(z[k]);
+                    o.store((T *)a.dz + row + at.c[k]);
+                }
+            } else if (a.silu) {
+#pragma unroll
+                for (int i = 0; i < HV; ++i) {
+                    const f32x2 n = fma2(v[k][i], w[k][i], b[k][i]);
+                    g[k][i] = mul2(g[k][i], silu_grad2(n, sigmoid2(n)));
+                }
             }
-            if (a.z && at.on[k] && m < a.M) {
-                z[k].set(dz);
-                z[k].store((T *)a.dz + row + at.c[k]);
+#pragma unroll
+            for (int i = 0; i < HV; ++i) {
+                dw[k][i] = fma2(g[k][i], v[k][i], dw[k][i]);
+                db[k][i] = add2(db[k][i], g[k][i]);
+                g[k][i] = mul2(g[k][i], w[k][i]);
+                s1 = add2(s1, g[k][i]);
+                s2 = fma2(g[k][i], v[k][i], s2);
             }
         }
-        s1 = a.center ? group_total(s1, p.lpg, sm) * inv_d : 0.f;
-        s2 = group_total(s2, p.lpg, sm) * inv_d;
+        float tot[2] = {sum2(s1), sum2(s2)};
+        group_totals(tot, p.lpg, sm);
+        const f32x2 m1 = both(a.center ? -tot[0] * inv_d : 0.f), m2 = both(-tot[1] * inv_d);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) g[k][c] = rstd * (g[k][c] - s1 - v[k][c] * s2);
+            for (int i = 0; i < HV; ++i) g[k][i] = mul2(both(rstd), fma2(v[k][i], m2, add2(g[k][i], m1)));
             if (at.on[k] && m < a.M) {
-                x[k].set(g[k]);
-                x[k].store((T *)a.dx + row + at.c[k]);
+                Pack<T, VEC> o;
+                o.set2(g[k]);
+                o.store((T *)a.dx + row + at.c[k]);
             }
         }
     }
@@ -258,10 +274,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
     // join the CTA's MB tokens and leave one row of partials: dw [H][d], db [H][d]
     const size_t HD = (size_t)a.H * a.d;
     float *part = a.part + (size_t)(blockIdx.x / p.nhb) * 2 * HD;
-    const int width = p.HB * p.lpg * VEC * K;          // one token's channels in the CTA
+    const int side = p.HB * p.lpg, width = side * VEC * K;             // threads and channels of one token in the CTA
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        float(&acc)[K][VEC] = which ? db : dw;
+        float acc[K][2 * HV];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < HV; ++i) unpk(which ? db[k][i] : dw[k][i], acc[k][2 * i], acc[k][2 * i + 1]);
         if (p.MB > 1) {
             __syncthreads();
             if (at.live && at.ml > 0)
@@ -269,15 +289,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
                 for (int k = 0; k < K; ++k)
 #pragma unroll
                     for (int c = 0; c < VEC; ++c)
-                        sp[(size_t)(at.ml - 1) * width + (k * VEC + c) * p.HB * p.lpg + threadIdx.x % (p.HB * p.lpg)] = acc[k][c];
+                        sp[(size_t)(at.ml - 1) * width + (k * VEC + c) * side + threadIdx.x % side] = acc[k][c];
             __syncthreads();
             if (at.live && at.ml == 0)
 #pragma unroll
                 for (int k = 0; k < K; ++k)
 #pragma unroll
                     for (int c = 0; c < VEC; ++c)
-                        for (int q = 0; q + 1 < p.MB; ++q)
-                            acc[k][c] += sp[(size_t)q * width + (k * VEC + c) * p.HB * p.lpg + threadIdx.x];
+                        for (int q = 0; q + 1 < p.MB; ++q) acc[k][c] += sp[(size_t)q * width + (k * VEC + c) * side + threadIdx.x];
         }
         if (at.ml == 0) {
 #pragma unroll
@@ -307,10 +326,10 @@ NormShape norm_shape(int M, int H, int d, int dtype, int ctas_per_sm) {
         s.K = 1;
     } else if (nv <= 128) {
         s.p.lpg = 32;
-        s.K = nv <= 64 ? 2 : 4;
+        s.K = nv <= 64 && s.vec > 1 ? 2 : 4;
     } else {
         s.p.lpg = kNormThreads;
-        s.K = nv <= kNormThreads ? 1 : nv <= 4 * kNormThreads ? 4 : nv <= 8 * kNormThreads ? 8 : 32;
+        s.K = nv <= kNormThreads && s.vec > 1 ? 1 : nv <= 4 * kNormThreads ? 4 : s.vec > 1 ? 8 : 32;
     }
     const int slots = kNormThreads / s.p.lpg;
     s.p.HB = H < slots ? H : slots;
@@ -333,12 +352,10 @@ template <typename T, int VEC, int K> void run_bwd(const NormArgs &a, const Norm
 template <typename T, int VEC> void run(bool back, const NormArgs &a, const NormShape &s, cudaStream_t st) {
 #define QD_NORM_K(k) back ? run_bwd<T, VEC, k>(a, s.p, st) : run_fwd<T, VEC, k>(a, s.p, st)
     if (s.K == 1) QD_NORM_K(1);
-    else if (s.K == 2) QD_NORM_K(2);
     else if (s.K == 4) QD_NORM_K(4);
-    else if constexpr (VEC <= 4) {
-        if (s.K == 8) QD_NORM_K(8);
-        else if constexpr (VEC == 1) QD_NORM_K(32);
-    }
+    else if constexpr (VEC == 1) QD_NORM_K(32);
+    else if (s.K == 2) QD_NORM_K(2);
+    else if constexpr (VEC == 4) QD_NORM_K(8);
 #undef QD_NORM_K
 }
 

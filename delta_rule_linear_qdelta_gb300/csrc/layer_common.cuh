@@ -30,10 +30,34 @@ template <typename T, int VEC> struct Pack {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) f[i] = to_f(e[i]);
     }
+    // the elements as (VEC + 1) / 2 pairs; a single element's other half is 0
+    __device__ __forceinline__ void get2(unsigned long long (&f)[(VEC + 1) / 2]) const {
+        float e[VEC + 1];
+        float(&g)[VEC] = *reinterpret_cast<float(*)[VEC]>(e);
+        get(g);
+        e[VEC] = 0.f;
+#pragma unroll
+        for (int i = 0; i < (VEC + 1) / 2; ++i)
+            asm("mov.b64 %0, {%1, %2};" : "=l"(f[i]) : "f"(e[2 * i]), "f"(e[2 * i + 1]));
+    }
+    __device__ __forceinline__ void set2(const unsigned long long (&f)[(VEC + 1) / 2]) {
+        float e[VEC + 1];
+#pragma unroll
+        for (int i = 0; i < (VEC + 1) / 2; ++i)
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(e[2 * i]), "=f"(e[2 * i + 1]) : "l"(f[i]));
+        const float(&g)[VEC] = *reinterpret_cast<const float(*)[VEC]>(e);
+        set(g);
+    }
     __device__ __forceinline__ void set(const float (&f)[VEC]) {
         T *e = reinterpret_cast<T *>(&bits);
+        if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {   // two at once: one conversion instruction
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) e[i] = from_f<T>(f[i]);
+            for (int i = 0; i < VEC; i += 2)
+                reinterpret_cast<__nv_bfloat162 *>(e)[i / 2] = __floats2bfloat162_rn(f[i], f[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) e[i] = from_f<T>(f[i]);
+        }
     }
 };
 
@@ -45,12 +69,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// sigmoid(x) = 1 / (1 + e^-x) with the approximate division (2 ulp), which returns 0 for a
-// divisor above 2^126: x < -87, where the sigmoid is below the normal range of fp32.
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + exp2_fast(-x * kLog2e)); }
-
-// d/dx SiLU(x), given s = sigmoid(x).
-__device__ __forceinline__ float silu_grad(float x, float s) { return s * fmaf(x, 1.f - s, 1.f); }
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Two fp32 numbers in one 64-bit register and the packed instructions on them, which issue
 // once for both.
@@ -87,6 +110,16 @@ __device__ __forceinline__ float sum2(f32x2 v) {
     return a + b;
 }
 
+// sigmoid(x) = 1 / (1 + e^-x) of two numbers; 0 where e^-x overflows.
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
+    const f32x2 d = add2(exp2_2(mul2(x, pk(-kLog2e, -kLog2e))), pk(1.f, 1.f));
+    float a, b;
+    unpk(d, a, b);
+    return pk(rcp_fast(a), rcp_fast(b));
+}
+// d/dx SiLU(x) = s + x s (1 - s), given s = sigmoid(x).
+__device__ __forceinline__ f32x2 silu_grad2(f32x2 x, f32x2 s) { return fma2(mul2(x, s), fma2(s, pk(-1.f, -1.f), pk(1.f, 1.f)), s); }
+
 // softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1], of two numbers.  log(1 + e) = e P(e)
 // with P the ninth-degree polynomial of least relative error on [0, 1] (5e-9, from an
 // iterated weighted least-squares fit); evaluated in fp32 it is within 1.4e-7, and a small
@@ -112,7 +145,15 @@ __device__ __forceinline__ void softplus2(float &x, float &y, float &ex, float &
     y = fmaxf(y, 0.f) + b;
 }
 // sigmoid(x), the derivative of softplus, from e = e^-|x|: nothing cancels on either side.
-__device__ __forceinline__ float softplus_grad(float x, float e) { return __fdividef(x >= 0.f ? 1.f : e, 1.f + e); }
+__device__ __forceinline__ float softplus_grad(float x, float e) { return (x >= 0.f ? 1.f : e) * rcp_fast(1.f + e); }
+
+// Asynchronous copy of BYTES to shared memory, or zeros where there is nothing to copy.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src, bool on) {
+    const unsigned to = (unsigned)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(BYTES), "r"(on ? BYTES : 0) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // Sum each of CNT values (a power of two) over the NL lanes that differ in the lane bits
 // STRIDE, 2 STRIDE, .., STRIDE NL / 2.  While a lane still holds several values it gives

@@ -7,58 +7,105 @@
 // All three are bound by memory: W + 4 operations per element against 4 to 12 bytes.  A
 // thread owns VEC neighbouring channels and walks a run of tokens with the last W - 1
 // inputs in registers, so x is read once but for the W - 1 tokens before (backward: and
-// after) each run, which neighbouring threads have just brought into the caches.
+// after) each run.  The tokens ahead arrive by asynchronous copies in a ring of shared memory
+// that only this thread uses: no barrier, and registers hold the filters, not the loads.
+#include <type_traits>
+
 #include "layer_common.cuh"
 
 namespace qd {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kBatch = 4;             // tokens in flight while as many are computed
+constexpr int kBatch = 4, kRing = 3;  // tokens computed together; batches in the ring
+constexpr int kFwdThreads = 128, kBwdThreads = 256, kStepThreads = 128;
+constexpr int kFwdCtas = 5, kBwdCtas = 2;    // resident on an SM
 
-// `rows` consecutive channels' filters, w[c * W + j]; 16-byte loads when VEC > 1.
-template <int VEC, int W> __device__ __forceinline__ void load_filter(const float *w, float (&f)[VEC][W]) {
+// The filters of VEC channels (w[c][j]) as pairs of channels per tap.
+template <int VEC, int W> __device__ __forceinline__ void load_filter(const float *w, f32x2 (&f)[W][(VEC + 1) / 2]) {
+    float flat[(VEC + 1) * W];
     if constexpr (VEC > 1) {
-        float flat[VEC * W];
 #pragma unroll
         for (int i = 0; i < VEC * W / 4; ++i) {
             const float4 v = reinterpret_cast<const float4 *>(w)[i];
             flat[4 * i] = v.x; flat[4 * i + 1] = v.y; flat[4 * i + 2] = v.z; flat[4 * i + 3] = v.w;
         }
-#pragma unroll
-        for (int c = 0; c < VEC; ++c)
-#pragma unroll
-            for (int j = 0; j < W; ++j) f[c][j] = flat[c * W + j];
     } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[0][j] = w[j];
+        for (int j = 0; j < W; ++j) {
+            flat[j] = w[j];
+            flat[W + j] = 0.f;
+        }
     }
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int i = 0; i < (VEC + 1) / 2; ++i) f[j][i] = pk(flat[2 * i * W + j], flat[(2 * i + 1) * W + j]);
+}
+template <int VEC> __device__ __forceinline__ void load_bias(const float *bias, int c0, f32x2 (&f)[(VEC + 1) / 2]) {
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i)
+        f[i] = bias ? pk(bias[c0 + 2 * i], 2 * i + 1 < VEC ? bias[c0 + 2 * i + 1] : 0.f) : 0;
 }
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int T) {
     return lens ? min(max(lens[b], 0), T) : T;
 }
 
+// One array's tokens ahead: slot u of batch i of this thread's ring, or zeros past `end`.  Single
+// 16-bit elements are below what a copy can move and are loaded when they are used.
+template <typename T, int VEC, int THREADS> struct Ahead {
+    using P = Pack<T, VEC>;
+    static constexpr bool ASYNC = VEC * sizeof(T) >= 4;
+    static constexpr size_t BYTES = ASYNC ? (size_t)kRing * kBatch * THREADS * VEC * sizeof(T) : 0;
+    __device__ __forceinline__ static T *slot(T *ring, int buf, int u) {
+        return ring + ((size_t)(buf * kBatch + u) * THREADS + threadIdx.x) * VEC;
+    }
+    __device__ __forceinline__ static void issue(T *ring, int buf, const T *src, int D, int t, int end) {
+        if constexpr (ASYNC) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                copy_async<VEC * sizeof(T)>(slot(ring, buf, u), t + u < end ? src + (size_t)(t + u) * D : src, t + u < end);
+        }
+    }
+    __device__ __forceinline__ static void get(T *ring, int buf, int u, const T *src, int D, int t, int end, f32x2 (&f)[(VEC + 1) / 2]) {
+        P v;
+        if constexpr (ASYNC) {
+            v.load(slot(ring, buf, u));
+        } else {
+            v.zero();
+            if (t + u < end) v.load(src + (size_t)(t + u) * D);
+        }
+        v.get2(f);
+    }
+};
+
 // Thread i: channel vector i % ncv, run i / ncv of the B * nruns runs of `run` tokens.  Run
 // 0 alone reads S0 (run >= W - 1) and afterwards writes S_final, so the two may be one buffer.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int run, int nruns) {
+__global__ void __launch_bounds__(kFwdThreads, kFwdCtas) conv_fwd_kernel(ConvArgs a, int run, int nruns) {
     using P = Pack<T, VEC>;
+    using In = Ahead<T, VEC, kFwdThreads>;
+    constexpr int HV = (VEC + 1) / 2;
+    extern __shared__ float4 smem4[];
+    T *ring = reinterpret_cast<T *>(smem4);
     const int ncv = a.D / VEC;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t i = (int64_t)blockIdx.x * kFwdThreads + threadIdx.x;
     if (i >= (int64_t)a.B * nruns * ncv) return;
     const int cv = (int)(i % ncv);
     const int64_t br = i / ncv;
     const int b = (int)(br / nruns), r = (int)(br % nruns);
     const int D = a.D, n = seq_len(a.lens, b, a.T), c0 = cv * VEC;
-    const int t0 = r * run, t1 = min(t0 + run, a.T);
+    const int t0 = (int)min((int64_t)r * run, (int64_t)a.T), t1 = min(t0 + run, a.T), end = min(t1, n);
     const T *x = (const T *)a.x + (size_t)b * a.T * D + c0;
     T *y = (T *)a.y + (size_t)b * a.T * D + c0;
 
-    float w[VEC][W], bias[VEC];
+    In::issue(ring, 0, x, D, t0, end);
+    copies_issued();
+    In::issue(ring, 1, x, D, t0 + kBatch, end);
+    copies_issued();
+    f32x2 w[W][HV], bias[HV];
     load_filter<VEC, W>(a.w + (size_t)c0 * W, w);
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) bias[c] = a.bias ? a.bias[c0 + c] : 0.f;
+    load_bias<VEC>(a.bias, c0, bias);
 
     P head[W - 1];                                     // the W - 1 inputs before t0
 #pragma unroll
@@ -71,42 +118,37 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int run,
             head[k].load((const T *)a.S0 + ((size_t)b * (W - 1) + (t + W - 1)) * D + c0);
         }
     }
-    float win[W][VEC];                                 // the inputs t - W + 1 .. t
+    f32x2 win[W][HV];                                  // the inputs t - W + 1 .. t
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) head[k].get(win[k + 1]);
+    for (int k = 0; k < W - 1; ++k) head[k].get2(win[k + 1]);
 
-    P in[kBatch], next[kBatch];
-    auto fetch = [&](P(&to)[kBatch], int t) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            to[u].zero();
-            if (t + u < t1 && t + u < n) to[u].load(x + (size_t)(t + u) * D);
-        }
-    };
-    fetch(next, t0);
-    for (int t = t0; t < t1; t += kBatch) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) in[u] = next[u];
-        fetch(next, t + kBatch);
+    int buf = 0;
+    for (int t = t0; t < t1; t += kBatch, buf = buf + 1 < kRing ? buf + 1 : 0) {
+        In::issue(ring, buf + 2 < kRing ? buf + 2 : buf + 2 - kRing, x, D, t + 2 * kBatch, end);
+        copies_issued();
+        copies_done<2>();
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) win[k][c] = win[k + 1][c];
-            in[u].get(win[W - 1]);
+                for (int h = 0; h < HV; ++h) win[k][h] = win[k + 1][h];
+            In::get(ring, buf, u, x, D, t, end, win[W - 1]);
+            f32x2 o[HV];
+#pragma unroll
+            for (int h = 0; h < HV; ++h) {
+                o[h] = bias[h];
+#pragma unroll
+                for (int j = 0; j < W; ++j) o[h] = fma2(w[j][h], win[j][h], o[h]);
+            }
+            if (a.silu) {
+#pragma unroll
+                for (int h = 0; h < HV; ++h) o[h] = mul2(o[h], sigmoid2(o[h]));
+            }
             if (t + u < t1) {
-                float o[VEC];
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    float p = bias[c];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(w[c][j], win[j][c], p);
-                    if (a.silu) p *= sigmoid_f(p);
-                    o[c] = t + u < n ? p : 0.f;
-                }
                 P out;
-                out.set(o);
+                out.set2(o);
+                if (t + u >= n) out.zero();
                 out.store(y + (size_t)(t + u) * D);
             }
         }
@@ -130,10 +172,11 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int run,
 }
 
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kStepThreads) conv_step_kernel(ConvArgs a) {
     using P = Pack<T, VEC>;
+    constexpr int HV = (VEC + 1) / 2;
     const int ncv = a.D / VEC;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t i = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
     if (i >= (int64_t)a.B * ncv) return;
     const int c0 = (int)(i % ncv) * VEC;
     const size_t b = (size_t)(i / ncv);
@@ -143,23 +186,22 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs a) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) in[k].load(S + (size_t)k * D);
     in[W - 1].load((const T *)a.x + b * D + c0);
-    float w[VEC][W], p[VEC];
+    f32x2 w[W][HV], p[HV];
     load_filter<VEC, W>(a.w + (size_t)c0 * W, w);
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) p[c] = a.bias ? a.bias[c0 + c] : 0.f;
+    load_bias<VEC>(a.bias, c0, p);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        float v[VEC];
-        in[j].get(v);
+        f32x2 v[HV];
+        in[j].get2(v);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) p[c] = fmaf(w[c][j], v[c], p[c]);
+        for (int h = 0; h < HV; ++h) p[h] = fma2(w[j][h], v[h], p[h]);
     }
     if (a.silu) {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) p[c] *= sigmoid_f(p[c]);
+        for (int h = 0; h < HV; ++h) p[h] = mul2(p[h], sigmoid2(p[h]));
     }
     P out;
-    out.set(p);
+    out.set2(p);
     out.store((T *)a.y + b * D + c0);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) in[k + 1].store(S + (size_t)k * D);
@@ -170,36 +212,38 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs a) {
 // the W pending dx (acc[j] belongs to token t - W + 1 + j; acc[0] is complete and leaves),
 // and, inside the run, to dw and dbias, which the CTA then sums over its runs in shared
 // memory and leaves as one row of partials ([D][W] of dw, then [D] of dbias).
-constexpr int kBwdThreads = 256;
-
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(ConvBwdArgs a, int CV, int run, int nrb, int ncb) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwdArgs a, int CV, int run, int nrb, int ncb) {
     using P = Pack<T, VEC>;
+    using In = Ahead<T, VEC, kBwdThreads>;
+    constexpr int HV = (VEC + 1) / 2;
+    extern __shared__ float4 smem4[];
+    T *rx = reinterpret_cast<T *>(smem4), *rg = rx + In::BYTES / sizeof(T);
     const int D = a.D, RB = kBwdThreads / CV;
     const int cvl = threadIdx.x % CV, rl = threadIdx.x / CV;
     const int cb = blockIdx.x % ncb, row = blockIdx.x / ncb;
     const int c0 = (cb * CV + cvl) * VEC;
     const int b = row / nrb, rb = row % nrb;
     const int r = rb * RB + rl;
-    const bool on = c0 < D;
     const int n = seq_len(a.lens, b, a.T);
-    const int64_t t0l = (int64_t)r * run;
-    const int t0 = (int)(t0l < a.T ? t0l : a.T), t1 = min(t0 + run, a.T);
+    const int t0 = (int)min((int64_t)r * run, (int64_t)a.T), t1 = min(t0 + run, a.T);
     const size_t base = (size_t)b * a.T * D + c0;
     const T *x = (const T *)a.x + base, *dy = (const T *)a.dy + base;
     T *dx = (T *)a.dx + base;
 
-    float w[VEC][W], bias[VEC], dw[VEC][W], db[VEC], win[W][VEC], acc[W][VEC];
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-        db[c] = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) dw[c][j] = acc[j][c] = win[j][c] = 0.f;
-    }
-    if (on && (t0 < t1 || r == 0)) {
+    f32x2 dw[W][HV] = {}, db[HV] = {};
+    if (c0 < D && (t0 < t1 || r == 0)) {
+        const int stop = t1 + W - 1, end = min(stop, n);       // tokens t1 .. stop - 1 complete the run's last dx
+        auto issue = [&](int t, int buf) {
+            In::issue(rx, buf, x, D, t, end);
+            In::issue(rg, buf, dy, D, t, end);
+            copies_issued();
+        };
+        issue(t0, 0);
+        issue(t0 + kBatch, 1);
+        f32x2 w[W][HV], bias[HV], win[W][HV], acc[W][HV] = {};
         load_filter<VEC, W>(a.w + (size_t)c0 * W, w);
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) bias[c] = a.bias ? a.bias[c0 + c] : 0.f;
+        load_bias<VEC>(a.bias, c0, bias);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             const int t = t0 - (W - 1) + k;
@@ -210,94 +254,96 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(ConvBwdArgs a, in
             } else if (a.S0) {
                 v.load((const T *)a.S0 + ((size_t)b * (W - 1) + (t + W - 1)) * D + c0);
             }
-            v.get(win[k + 1]);
+            v.get2(win[k + 1]);
         }
-        const int end = t1 + W - 1;                    // tokens t1 .. end - 1 complete the run's last dx
-        P xi[kBatch], gi[kBatch], xn[kBatch], gn[kBatch];
-        auto fetch = [&](int t) {
+        int buf = 0;
+        // One token; INSIDE: it and its W - 1 predecessors are plain tokens of this run.
+        auto token = [&](auto inside, int t, int u) {
+            constexpr bool INSIDE = decltype(inside)::value;
+            const int tt = t + u, s = tt - (W - 1);
+            f32x2 g[HV];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                xn[u].zero();
-                gn[u].zero();
-                if (t + u < end && t + u < n) {
-                    xn[u].load(x + (size_t)(t + u) * D);
-                    gn[u].load(dy + (size_t)(t + u) * D);
+            for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                for (int h = 0; h < HV; ++h) win[k][h] = win[k + 1][h];
+            In::get(rx, buf, u, x, D, t, end, win[W - 1]);
+            In::get(rg, buf, u, dy, D, t, end, g);
+            if (a.silu) {
+#pragma unroll
+                for (int h = 0; h < HV; ++h) {
+                    f32x2 p = bias[h];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) p = fma2(w[j][h], win[j][h], p);
+                    g[h] = mul2(g[h], silu_grad2(p, sigmoid2(p)));
                 }
             }
+            if (!INSIDE && tt >= n) {
+#pragma unroll
+                for (int h = 0; h < HV; ++h) g[h] = 0;
+            }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int h = 0; h < HV; ++h) acc[j][h] = fma2(w[j][h], g[h], acc[j][h]);
+            if (INSIDE || tt < t1) {
+#pragma unroll
+                for (int h = 0; h < HV; ++h) {
+                    db[h] = add2(db[h], g[h]);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][h] = fma2(g[h], win[j][h], dw[j][h]);
+                }
+            }
+            // token s is complete: it is this run's, or (run 0) a row of S0
+            if (INSIDE || (tt < stop && (s >= t0 || r == 0))) {
+                f32x2 o[HV];
+#pragma unroll
+                for (int h = 0; h < HV; ++h) o[h] = acc[0][h];
+                const int kf = s - (n - (W - 1));              // its row in S_final, if any
+                if (!INSIDE && a.dS_final && kf >= 0 && kf < W - 1) {
+                    P v;
+                    f32x2 f[HV];
+                    v.load((const T *)a.dS_final + ((size_t)b * (W - 1) + kf) * D + c0);
+                    v.get2(f);
+#pragma unroll
+                    for (int h = 0; h < HV; ++h) o[h] = add2(o[h], f[h]);
+                }
+                P out;
+                out.set2(o);
+                if (INSIDE || s >= 0) out.store(dx + (size_t)s * D);
+                else if (a.dS0) out.store((T *)a.dS0 + ((size_t)b * (W - 1) + (s + W - 1)) * D + c0);
+            }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int h = 0; h < HV; ++h) acc[j][h] = j + 1 < W ? acc[j + 1 < W ? j + 1 : j][h] : 0;
         };
-        fetch(t0);
-        for (int t = t0; t < end; t += kBatch) {
+        for (int t = t0; t < stop; t += kBatch, buf = buf + 1 < kRing ? buf + 1 : 0) {
+            issue(t + 2 * kBatch, buf + 2 < kRing ? buf + 2 : buf + 2 - kRing);
+            copies_done<2>();
+            if (t >= t0 + W - 1 && t + kBatch <= min(t1, n)) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                xi[u] = xn[u];
-                gi[u] = gn[u];
-            }
-            fetch(t + kBatch);
+                for (int u = 0; u < kBatch; ++u) token(std::true_type{}, t, u);
+            } else {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int tt = t + u;
-                if (tt < end) {
-                    float g[VEC];
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                        for (int c = 0; c < VEC; ++c) win[k][c] = win[k + 1][c];
-                    xi[u].get(win[W - 1]);
-                    gi[u].get(g);
-#pragma unroll
-                    for (int c = 0; c < VEC; ++c) {
-                        if (a.silu) {
-                            float p = bias[c];
-#pragma unroll
-                            for (int j = 0; j < W; ++j) p = fmaf(w[c][j], win[j][c], p);
-                            g[c] *= silu_grad(p, sigmoid_f(p));
-                        }
-                        if (tt >= n) g[c] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) acc[j][c] = fmaf(w[c][j], g[c], acc[j][c]);
-                        if (tt < t1) {
-                            db[c] += g[c];
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dw[c][j] = fmaf(g[c], win[j][c], dw[c][j]);
-                        }
-                    }
-                    // token s = tt - (W - 1) is complete: it is this run's, or (run 0) a row of S0
-                    const int s = tt - (W - 1);
-                    if (s >= t0 || r == 0) {
-                        float o[VEC];
-                        const int kf = s - (n - (W - 1));          // its row in S_final, if any
-#pragma unroll
-                        for (int c = 0; c < VEC; ++c) o[c] = acc[0][c];
-                        if (a.dS_final && kf >= 0 && kf < W - 1) {
-                            P v;
-                            float f[VEC];
-                            v.load((const T *)a.dS_final + ((size_t)b * (W - 1) + kf) * D + c0);
-                            v.get(f);
-#pragma unroll
-                            for (int c = 0; c < VEC; ++c) o[c] += f[c];
-                        }
-                        P out;
-                        out.set(o);
-                        if (s >= 0) out.store(dx + (size_t)s * D);
-                        else if (a.dS0) out.store((T *)a.dS0 + ((size_t)b * (W - 1) + (s + W - 1)) * D + c0);
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-#pragma unroll
-                        for (int c = 0; c < VEC; ++c) acc[j][c] = j + 1 < W ? acc[j + 1 < W ? j + 1 : j][c] : 0.f;
-                }
+                for (int u = 0; u < kBatch; ++u) token(std::false_type{}, t, u);
             }
         }
+        copies_done<0>();
     }
     // sum the CTA's runs: [run][channel vector][VEC * (W + 1)], then one thread per column
     constexpr int C = VEC * (W + 1);
-    extern __shared__ float sp[];
+    float *sp = reinterpret_cast<float *>(smem4);
+    __syncthreads();                                           // every ring is read out
     float *mine = sp + (size_t)(rl * CV + cvl) * C;
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) {
+    for (int h = 0; h < HV; ++h) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) mine[c * W + j] = dw[c][j];
-        mine[VEC * W + c] = db[c];
+        for (int j = 0; j <= W; ++j) {
+            float lo, hi;
+            unpk(j < W ? dw[j < W ? j : 0][h] : db[h], lo, hi);
+            mine[j < W ? 2 * h * W + j : VEC * W + 2 * h] = lo;
+            if (2 * h + 1 < VEC) mine[j < W ? (2 * h + 1) * W + j : VEC * W + 2 * h + 1] = hi;
+        }
     }
     __syncthreads();
     float *part = a.part + (size_t)row * D * (W + 1);
@@ -311,20 +357,33 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(ConvBwdArgs a, in
     }
 }
 
+// The run (a multiple of the batch) of the least time: rounds of `slots` resident CTAs, each
+// as long as a run and what it costs beside its tokens (`extra`: overlap, filters, first copies).
+template <typename F> int best_run(int T, int64_t slots, int extra, F ctas) {
+    int best = kBatch;
+    int64_t least = INT64_MAX;
+    for (int run = kBatch; run <= 256 && run < T + kBatch; run += kBatch) {
+        const int64_t cost = (ctas(run) + slots - 1) / slots * (run + extra);
+        if (cost < least) {
+            least = cost;
+            best = run;
+        }
+    }
+    return best;
+}
+
 template <typename T, int VEC, int W> void run_fwd(const ConvArgs &a, cudaStream_t s) {
-    // The longest run (16, 8 or 4 tokens) that still leaves about 1024 threads per SM: a
-    // longer run reads its W - 1 tokens of overlap less often, more threads keep more loads
-    // in flight.
     const int64_t vecs = (int64_t)a.B * (a.D / VEC);
-    int run = 16;
-    while (run > 4 && vecs * ((a.T + run - 1) / run) < (int64_t)kSMs * 1024) run /= 2;
+    auto ctas = [&](int run) { return (vecs * ((a.T + run - 1) / run) + kFwdThreads - 1) / kFwdThreads; };
+    const int run = best_run(a.T, kFwdCtas * kSMs, 12, ctas);
     const int nruns = a.T > 0 ? (a.T + run - 1) / run : 1;
     const int64_t n = vecs * nruns;
-    conv_fwd_kernel<T, VEC, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, run, nruns);
+    conv_fwd_kernel<T, VEC, W><<<(unsigned)((n + kFwdThreads - 1) / kFwdThreads), kFwdThreads,
+                                 Ahead<T, VEC, kFwdThreads>::BYTES, s>>>(a, run, nruns);
 }
 template <typename T, int VEC, int W> void run_step(const ConvArgs &a, cudaStream_t s) {
     const int64_t n = (int64_t)a.B * (a.D / VEC);
-    conv_step_kernel<T, VEC, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+    conv_step_kernel<T, VEC, W><<<(unsigned)((n + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(a);
 }
 
 struct BwdPlan {
@@ -340,18 +399,22 @@ BwdPlan bwd_plan(int B, int T, int D) {
     p.CV = 32;
     while (p.CV > 1 && p.CV / 2 >= ncv) p.CV /= 2;
     const int RB = kBwdThreads / p.CV;
-    p.run = 32;
-    const int64_t cols = (int64_t)B * ((ncv + p.CV - 1) / p.CV);
-    while (p.run > 4 && cols * ((T + p.run * RB - 1) / (p.run * RB)) < 2 * kSMs) p.run /= 2;
-    p.nrb = T > 0 ? (T + p.run * RB - 1) / (p.run * RB) : 1;
     p.ncb = (ncv + p.CV - 1) / p.CV;
+    p.run = best_run(T, kBwdCtas * kSMs, 24, [&](int run) { return (int64_t)B * p.ncb * ((T + run * RB - 1) / (run * RB)); });
+    p.nrb = T > 0 ? (T + p.run * RB - 1) / (p.run * RB) : 1;
     p.rows = B * p.nrb;
     return p;
 }
 
-template <typename T, int VEC, int W> void run_bwd(const ConvBwdArgs &a, const BwdPlan &p, cudaStream_t s) {
-    conv_bwd_kernel<T, VEC, W><<<(unsigned)p.ncb * p.rows, kBwdThreads, kBwdThreads * VEC * (W + 1) * sizeof(float), s>>>(
-        a, p.CV, p.run, p.nrb, p.ncb);
+template <typename T, int VEC, int W> cudaError_t run_bwd(const ConvBwdArgs &a, const BwdPlan &p, cudaStream_t s) {
+    const size_t ring = 2 * Ahead<T, VEC, kBwdThreads>::BYTES, sums = kBwdThreads * VEC * (W + 1) * sizeof(float);
+    const size_t smem = ring > sums ? ring : sums;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, VEC, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    conv_bwd_kernel<T, VEC, W><<<(unsigned)p.ncb * p.rows, kBwdThreads, smem, s>>>(a, p.CV, p.run, p.nrb, p.ncb);
+    return cudaGetLastError();
 }
 
 template <typename T_, int VEC_, int W_> struct Inst {
@@ -401,9 +464,10 @@ size_t conv_bwd_workspace(int B, int T, int D, int W) {
 cudaError_t launch_conv_bwd(const ConvBwdArgs &a, int dtype, cudaStream_t s, int *nlaunch) {
     const BwdPlan p = bwd_plan(a.B, a.T, a.D);
     if (p.rows > 0) {
-        with_inst<4>(dtype, a.D, a.W, [&](auto i) { run_bwd<typename decltype(i)::T, i.VEC, i.W>(a, p, s); });
-        const cudaError_t e = launched(nlaunch);
+        cudaError_t e = cudaSuccess;
+        with_inst<4>(dtype, a.D, a.W, [&](auto i) { e = run_bwd<typename decltype(i)::T, i.VEC, i.W>(a, p, s); });
         if (e != cudaSuccess) return e;
+        *nlaunch += 1;
     }
     return launch_sum_rows(a.part, p.rows, (int64_t)a.D * (a.W + 1), a.dw, (int64_t)a.D * a.W, a.dbias, a.D, nullptr, s,
                            nlaunch);

@@ -16,65 +16,90 @@ using namespace ssm;
 constexpr int kStepThreads = 256;
 
 // One token: the state is read once and written once, everything else is small.  A thread
-// takes four states of a channel (one at a time when N is no multiple of four).
-template <typename T, int LN, int SPL>
+// takes states 4 i + 0..3, i = ln, ln + LN, .. of one channel (SPL of them; N no multiple of four: one by
+// one) for kSeqs sequences, so A is read once for all of them and their states are in
+// flight together.
+constexpr int kSeqs = 4;
+
+template <typename T, int LN, int SPL, bool WIDE>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmArgs a, int per_group) {
-    constexpr int CPB = kStepThreads / LN;
+    constexpr int CPB = kStepThreads / LN, Q = SPL / 4;
     const int64_t nblk = (a.D + CPB - 1) / CPB;
-    const size_t b = blockIdx.x / nblk;
+    const int64_t b0 = blockIdx.x / nblk * kSeqs;
     const int ln = threadIdx.x % LN, ch = threadIdx.x / LN, lane = threadIdx.x & 31;
     const int d = (int)(blockIdx.x % nblk) * CPB + ch, N = a.N;
     const bool live = d < a.D;
-    float acc = 0.f, x = 0.f;
-    if (live) {
-        const size_t bd = b * a.D + d;
-        x = to_f(((const T *)a.x)[bd]);
-        float u = to_f(((const T *)a.delta)[bd]) + (a.delta_bias ? a.delta_bias[d] : 0.f);
-        if (a.softplus) {
-            float none = 0.f, e0, e1;
-            softplus2(u, none, e0, e1);
+    const int seqs = live ? (int)min((int64_t)kSeqs, a.B - b0) : 0;
+    const int grp = live ? d / per_group : 0;
+    const float bias = live && a.delta_bias ? a.delta_bias[d] : 0.f, skip = live && a.Dskip ? a.Dskip[d] : 0.f;
+    float u[kSeqs], x[kSeqs], acc[kSeqs];
+    float4 s[WIDE ? kSeqs : 1][Q];
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < kSeqs; ++j)
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const int k = (i * LN + ln) * 4;
+                if (j < seqs && k < N) s[j][i] = *reinterpret_cast<const float4 *>(a.S_final + ((b0 + j) * a.D + d) * N + k);
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        const size_t bd = (b0 + (j < seqs ? j : 0)) * a.D + (live ? d : 0);
+        x[j] = to_f(((const T *)a.x)[bd]);
+        u[j] = to_f(((const T *)a.delta)[bd]) + bias;
+        acc[j] = 0.f;
+    }
+    if (a.softplus) {
+        float e0, e1;
+#pragma unroll
+        for (int j = 0; j < kSeqs; j += 2) softplus2(u[j], u[j + 1], e0, e1);
+    }
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            const int k = (i * LN + ln) * 4;
+            if (k >= N || !live) continue;
+            float4 A = *reinterpret_cast<const float4 *>(a.A + (size_t)d * N + k);
+            A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
+#pragma unroll
+            for (int j = 0; j < kSeqs; ++j) {
+                if (j >= seqs) continue;
+                const size_t at = ((b0 + j) * a.G + grp) * N + k;
+                Pack<T, 4> Bv, Cv;
+                float B[4], C[4];
+                Bv.load((const T *)a.Bm + at);
+                Cv.load((const T *)a.Cm + at);
+                Bv.get(B);
+                Cv.get(C);
+                const float ux = u[j] * x[j];
+                float4 &h = s[j][i];
+                h.x = fmaf(exp2_fast(u[j] * A.x), h.x, ux * B[0]);
+                h.y = fmaf(exp2_fast(u[j] * A.y), h.y, ux * B[1]);
+                h.z = fmaf(exp2_fast(u[j] * A.z), h.z, ux * B[2]);
+                h.w = fmaf(exp2_fast(u[j] * A.w), h.w, ux * B[3]);
+                acc[j] += h.x * C[0] + h.y * C[1] + h.z * C[2] + h.w * C[3];
+                *reinterpret_cast<float4 *>(a.S_final + ((b0 + j) * a.D + d) * N + k) = h;
+            }
         }
-        const float ux = u * x;
-        const size_t grp = (b * a.G + d / per_group) * N;
-        const T *Bp = (const T *)a.Bm + grp, *Cp = (const T *)a.Cm + grp;
-        float *S = a.S_final + bd * N;
-        const float *A = a.A + (size_t)d * N;
-        if (N % 4 == 0) {
-            float4 s[SPL / 4];
+    } else {
 #pragma unroll
-            for (int i = 0; i < SPL / 4; ++i) {
-                const int k = (i * LN + ln) * 4;
-                if (k < N) s[i] = *reinterpret_cast<const float4 *>(S + k);
-            }
-#pragma unroll
-            for (int i = 0; i < SPL / 4; ++i) {
-                const int k = (i * LN + ln) * 4;
-                if (k < N) {
-                    const float4 Av = *reinterpret_cast<const float4 *>(A + k);
-                    Pack<T, 4> Bv, Cv;
-                    float Bf[4], Cf[4];
-                    Bv.load(Bp + k);
-                    Cv.load(Cp + k);
-                    Bv.get(Bf);
-                    Cv.get(Cf);
-                    s[i].x = fmaf(exp2_fast(u * (Av.x * kLog2e)), s[i].x, ux * Bf[0]);
-                    s[i].y = fmaf(exp2_fast(u * (Av.y * kLog2e)), s[i].y, ux * Bf[1]);
-                    s[i].z = fmaf(exp2_fast(u * (Av.z * kLog2e)), s[i].z, ux * Bf[2]);
-                    s[i].w = fmaf(exp2_fast(u * (Av.w * kLog2e)), s[i].w, ux * Bf[3]);
-                    acc += s[i].x * Cf[0] + s[i].y * Cf[1] + s[i].z * Cf[2] + s[i].w * Cf[3];
-                    *reinterpret_cast<float4 *>(S + k) = s[i];
-                }
-            }
-        } else {
+        for (int j = 0; j < kSeqs; ++j) {
+            if (j >= seqs) continue;
+            const T *Bp = (const T *)a.Bm + ((b0 + j) * a.G + grp) * N, *Cp = (const T *)a.Cm + ((b0 + j) * a.G + grp) * N;
+            float *S = a.S_final + ((b0 + j) * a.D + d) * N;
             for (int k = ln; k < N; k += LN) {
-                const float s = fmaf(exp2_fast(u * (A[k] * kLog2e)), S[k], ux * to_f(Bp[k]));
-                acc = fmaf(s, to_f(Cp[k]), acc);
-                S[k] = s;
+                const float h = fmaf(exp2_fast(u[j] * (a.A[(size_t)d * N + k] * kLog2e)), S[k], u[j] * x[j] * to_f(Bp[k]));
+                acc[j] = fmaf(h, to_f(Cp[k]), acc[j]);
+                S[k] = h;
             }
         }
     }
-    lane_reduce<1, LN, 1>(&acc, lane);
-    if (live && ln == 0) ((T *)a.y)[b * a.D + d] = from_f<T>(acc + (a.Dskip ? a.Dskip[d] * x : 0.f));
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        lane_reduce<1, LN, 1>(acc + j, lane);
+        if (j < seqs && ln == 0) ((T *)a.y)[(b0 + j) * a.D + d] = from_f<T>(fmaf(skip, x[j], acc[j]));
+    }
 }
 
 // Segments: none while every SM has a CTA (256 CTAs of 8 x 2048 tokens x 2048 channels: 275 us
@@ -99,8 +124,9 @@ template <typename T> cudaError_t run_fwd(const SsmArgs &a, cudaStream_t s, int 
 }
 
 template <typename T, int LN, int SPL> cudaError_t run_step(const SsmArgs &a, cudaStream_t s, int *nlaunch) {
-    const int64_t blocks = (int64_t)a.B * ((a.D + kStepThreads / LN - 1) / (kStepThreads / LN));
-    step_kernel<T, LN, SPL><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, a.D / a.G);
+    const int64_t blocks = ((int64_t)a.B + kSeqs - 1) / kSeqs * ((a.D + kStepThreads / LN - 1) / (kStepThreads / LN));
+    if (a.N % 4 == 0) step_kernel<T, LN, SPL, true><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, a.D / a.G);
+    else step_kernel<T, LN, SPL, false><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, a.D / a.G);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) *nlaunch += 1;
     return e;

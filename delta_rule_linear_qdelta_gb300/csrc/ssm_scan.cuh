@@ -80,14 +80,6 @@ template <int VEC> __device__ __forceinline__ void step_sizes(float (&u)[VEC], c
     }
 }
 
-// Asynchronous copy of BYTES to shared memory, or zeros where there is nothing to copy.
-template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src, bool on) {
-    const unsigned to = (unsigned)__cvta_generic_to_shared(dst);
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(BYTES), "r"(on ? BYTES : 0) : "memory");
-}
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT> __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
-
 // A tile of tokens on its way from global to shared memory: NA token arrays and B and C.  The raw
 // tile arrives by asynchronous copies, two tiles ahead, in one of kStages buffers; every thread
 // then reads back what it copied itself (so its own wait is enough), converts it and stages it

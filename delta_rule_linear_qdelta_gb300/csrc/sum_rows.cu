@@ -1,12 +1,12 @@
 // Sums the rows of a matrix of partial results.  Memory bound: each partial is read once.
-// A CTA takes 32 columns; its 16 warps take every 16th row each, four loads in flight, and
+// A CTA takes 32 columns; its 32 warps take every 32nd row each, eight loads in flight, and
 // join through shared memory, so the order of the additions depends on P alone.
 #include "layer_common.cuh"
 
 namespace qd {
 namespace {
 
-constexpr int kRows = 16;
+constexpr int kRows = 32;
 
 __global__ void __launch_bounds__(32 * kRows) sum_rows_kernel(const float *part, int P, int64_t M, float *out1,
                                                               int64_t M1, float *out2, int64_t M2, float *out3) {
@@ -15,7 +15,7 @@ __global__ void __launch_bounds__(32 * kRows) sum_rows_kernel(const float *part,
     const int64_t m = (int64_t)blockIdx.x * 32 + lane;
     float acc = 0.f;
     if (m < M) {
-#pragma unroll 4
+#pragma unroll 8
         for (int p = row; p < P; p += kRows) acc += part[p * M + m];
     }
     s[row][lane] = acc;
