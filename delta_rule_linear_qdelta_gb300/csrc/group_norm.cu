@@ -22,17 +22,20 @@ struct NormPlan {
     int lpg, HB, MB, nhb, gm;
 };
 
-template <int CNT> __device__ __forceinline__ void group_totals(float (&v)[CNT], int lpg, float *sm) {
+// LPG: the threads of a group (a power of two up to 32, or the whole CTA), or 0 where only the
+// plan knows (up to 32).
+template <int LPG, int CNT> __device__ __forceinline__ void group_totals(float (&v)[CNT], int lpg, float *sm) {
+    const int n = LPG ? LPG : lpg;
     auto join = [&](int o) {
 #pragma unroll
         for (int i = 0; i < CNT; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     };
-    if (lpg > 16) join(16);
-    if (lpg > 8) join(8);
-    if (lpg > 4) join(4);
-    if (lpg > 2) join(2);
-    if (lpg > 1) join(1);
-    if (lpg > 32) {
+    if (n > 16) join(16);
+    if (n > 8) join(8);
+    if (n > 4) join(4);
+    if (n > 2) join(2);
+    if (n > 1) join(1);
+    if (LPG > 32) {
         __syncthreads();                               // the last totals have been read by all
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
@@ -89,7 +92,7 @@ template <int VEC, int K> struct Place {
 };
 
 // xh of the thread's channels of one group, and the group's rstd.
-template <int VEC, int K, int HV>
+template <int VEC, int K, int LPG, int HV>
 __device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K], const NormArgs &a, float inv_d, int lpg, float *sm) {
     if (a.center) {
         f32x2 s = 0;
@@ -98,7 +101,7 @@ __device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K
 #pragma unroll
             for (int i = 0; i < HV; ++i) s = add2(s, v[k][i]);
         float tot[1] = {sum2(s)};
-        group_totals(tot, lpg, sm);
+        group_totals<LPG>(tot, lpg, sm);
         const float m = -tot[0] * inv_d;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -111,8 +114,10 @@ __device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K
 #pragma unroll
         for (int i = 0; i < HV; ++i) q = fma2(v[k][i], v[k][i], q);
     float tot[1] = {sum2(q)};
-    group_totals(tot, lpg, sm);
-    const float rstd = 1.f / sqrtf(fmaf(tot[0], inv_d, a.eps));
+    group_totals<LPG>(tot, lpg, sm);
+    // the hardware's reciprocal root (2 ulp) and one Newton step
+    const float var = fmaf(tot[0], inv_d, a.eps), r0 = rsqrtf(var);
+    const float rstd = r0 * fmaf(-0.5f * var * r0, r0, 1.5f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -120,7 +125,7 @@ __device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K
     return rstd;
 }
 
-template <typename T, int VEC, int K>
+template <typename T, int VEC, int K, int LPG>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, NormPlan p) {
     constexpr int HV = (VEC + 1) / 2;
     __shared__ float sm[kNormThreads / 32];
@@ -130,9 +135,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
     at.param(a.b, a.d, 0.f, b);
     const float inv_d = 1.f / (float)a.d;
     const int64_t first = (int64_t)(blockIdx.x / p.nhb) * p.MB, turn = (int64_t)p.gm * p.MB;
+    const size_t step = (size_t)turn * a.H * a.d;
+    size_t row = ((size_t)(first + at.ml) * a.H + at.h) * a.d;
     Pack<T, VEC> xn[K], zn[K];
-    auto fetch = [&](int64_t m) {
-        const size_t row = ((size_t)m * a.H + at.h) * a.d;
+    auto fetch = [&](int64_t m, size_t row) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             xn[k].zero();
@@ -143,19 +149,18 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
             }
         }
     };
-    fetch(first + at.ml);
+    fetch(first + at.ml, row);
     // every thread of the CTA makes the same number of turns: the group totals synchronise
-    for (int64_t m0 = first; m0 < a.M; m0 += turn) {
+    for (int64_t m0 = first; m0 < a.M; m0 += turn, row += step) {
         const int64_t m = m0 + at.ml;
-        const size_t row = ((size_t)m * a.H + at.h) * a.d;
         f32x2 v[K][HV], t[K][HV];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             xn[k].get2(v[k]);
             zn[k].get2(t[k]);
         }
-        fetch(m + turn);                               // the next token's, while this one is computed
-        normalise<VEC, K, HV>(v, at.on, a, inv_d, p.lpg, sm);
+        fetch(m + turn, row + step);                   // the next token's, while this one is computed
+        normalise<VEC, K, LPG, HV>(v, at.on, a, inv_d, p.lpg, sm);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -180,8 +185,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
     }
 }
 
-template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, NormPlan p) {
+template <typename T, int VEC, int K, int LPG>
+__global__ void __launch_bounds__(kNormThreads, K == 1 && LPG <= 32 ? 3 : 1) norm_bwd_kernel(NormArgs a, NormPlan p) {
     constexpr int HV = (VEC + 1) / 2;
     __shared__ float sm[2 * kNormThreads / 32];
     extern __shared__ float sp[];
@@ -191,9 +196,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
     at.param(a.b, a.d, 0.f, b);
     const float inv_d = 1.f / (float)a.d;
     const int64_t begin = (int64_t)(blockIdx.x / p.nhb) * p.MB, turn = (int64_t)p.gm * p.MB;
+    const size_t step = (size_t)turn * a.H * a.d;
+    size_t row = ((size_t)(begin + at.ml) * a.H + at.h) * a.d;
     Pack<T, VEC> xn[K], zn[K], dyn[K];
-    auto fetch = [&](int64_t m) {
-        const size_t row = ((size_t)m * a.H + at.h) * a.d;
+    auto fetch = [&](int64_t m, size_t row) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             xn[k].zero();
@@ -206,10 +212,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
             }
         }
     };
-    fetch(begin + at.ml);
-    for (int64_t m0 = begin; m0 < a.M; m0 += turn) {
+    fetch(begin + at.ml, row);
+    for (int64_t m0 = begin; m0 < a.M; m0 += turn, row += step) {
         const int64_t m = m0 + at.ml;
-        const size_t row = ((size_t)m * a.H + at.h) * a.d;
         f32x2 v[K][HV], g[K][HV], z[K][HV];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -217,8 +222,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
             dyn[k].get2(g[k]);
             zn[k].get2(z[k]);
         }
-        fetch(m + turn);
-        const float rstd = normalise<VEC, K, HV>(v, at.on, a, inv_d, p.lpg, sm);
+        fetch(m + turn, row + step);
+        const float rstd = normalise<VEC, K, LPG, HV>(v, at.on, a, inv_d, p.lpg, sm);
         f32x2 s1 = 0, s2 = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormArgs a, Norm
             }
         }
         float tot[2] = {sum2(s1), sum2(s2)};
-        group_totals(tot, p.lpg, sm);
+        group_totals<LPG>(tot, p.lpg, sm);
         const f32x2 m1 = both(a.center ? -tot[0] * inv_d : 0.f), m2 = both(-tot[1] * inv_d);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -342,20 +347,24 @@ NormShape norm_shape(int M, int H, int d, int dtype, int ctas_per_sm) {
     return s;
 }
 
-template <typename T, int VEC, int K> void run_fwd(const NormArgs &a, const NormPlan &p, cudaStream_t s) {
-    norm_fwd_kernel<T, VEC, K><<<(unsigned)(p.gm * p.nhb), kNormThreads, 0, s>>>(a, p);
+template <typename T, int VEC, int K, int LPG> void run_fwd(const NormArgs &a, const NormPlan &p, cudaStream_t s) {
+    norm_fwd_kernel<T, VEC, K, LPG><<<(unsigned)(p.gm * p.nhb), kNormThreads, 0, s>>>(a, p);
 }
-template <typename T, int VEC, int K> void run_bwd(const NormArgs &a, const NormPlan &p, cudaStream_t s) {
+template <typename T, int VEC, int K, int LPG> void run_bwd(const NormArgs &a, const NormPlan &p, cudaStream_t s) {
     const size_t smem = (size_t)(p.MB - 1) * p.HB * p.lpg * VEC * K * sizeof(float);
-    norm_bwd_kernel<T, VEC, K><<<(unsigned)(p.gm * p.nhb), kNormThreads, smem, s>>>(a, p);
+    norm_bwd_kernel<T, VEC, K, LPG><<<(unsigned)(p.gm * p.nhb), kNormThreads, smem, s>>>(a, p);
 }
 template <typename T, int VEC> void run(bool back, const NormArgs &a, const NormShape &s, cudaStream_t st) {
-#define QD_NORM_K(k) back ? run_bwd<T, VEC, k>(a, s.p, st) : run_fwd<T, VEC, k>(a, s.p, st)
-    if (s.K == 1) QD_NORM_K(1);
-    else if (s.K == 4) QD_NORM_K(4);
-    else if constexpr (VEC == 1) QD_NORM_K(32);
-    else if (s.K == 2) QD_NORM_K(2);
-    else if constexpr (VEC == 4) QD_NORM_K(8);
+#define QD_NORM_K(k, l) back ? run_bwd<T, VEC, k, l>(a, s.p, st) : run_fwd<T, VEC, k, l>(a, s.p, st)
+    const bool whole = s.p.lpg == kNormThreads;        // a group per CTA
+    if (s.K == 1 && whole) QD_NORM_K(1, kNormThreads);
+    else if (s.K == 1 && VEC > 1 && s.p.lpg == 16) QD_NORM_K(1, 16);
+    else if (s.K == 1) QD_NORM_K(1, 0);
+    else if (s.K == 4 && whole) QD_NORM_K(4, kNormThreads);
+    else if (s.K == 4) QD_NORM_K(4, 32);
+    else if constexpr (VEC == 1) QD_NORM_K(32, kNormThreads);
+    else if (s.K == 2) QD_NORM_K(2, 32);
+    else if constexpr (VEC == 4) QD_NORM_K(8, kNormThreads);
 #undef QD_NORM_K
 }
 

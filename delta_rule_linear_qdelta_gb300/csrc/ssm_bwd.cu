@@ -145,14 +145,14 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
                 f32x2 r[2];
                 fetch(w.R, s * all + bd, c, r);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) dh[c][p] = fma2(exp2_2(mul2(pk(U, U), A2[c][p])), dh[c][p], r[p]);
+                for (int p = 0; p < 2; ++p) dh[c][p] = fma2(decay2(pk(U, U), A2[c][p]), dh[c][p], r[p]);
             }
             for (int s = 0; s < seg; ++s) {
                 const float U = ws[w.U + s * all + bd + c];
                 f32x2 e[2];
                 fetch(w.E, s * all + bd, c, e);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) hin[c][p] = fma2(exp2_2(mul2(pk(U, U), A2[c][p])), hin[c][p], e[p]);
+                for (int p = 0; p < 2; ++p) hin[c][p] = fma2(decay2(pk(U, U), A2[c][p]), hin[c][p], e[p]);
             }
         }
     }
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
         for (int tc = kTile - kChunk; tc >= 0; tc -= kChunk) {
             if (t0 + tc >= t_end) continue;                            // uniform over the CTA
             f32x2 h0[2][2], hh[kChunk][2][2], dAt[2][2] = {};
+            float dbt = 0.f, dDt = 0.f;                                // a chunk's share: short sums lose less
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const bool on = c0 + c < cb.count;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
                 if (seg > 0) {
                     const float U = on ? ck_u[c] : 0.f;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) h0[c][p] = fma2(exp2_2(mul2(pk(U, U), A2[c][p])), hin[c][p], h0[c][p]);
+                    for (int p = 0; p < 2; ++p) h0[c][p] = fma2(decay2(pk(U, U), A2[c][p]), hin[c][p], h0[c][p]);
                 }
             }
             if (t0 + tc > t_begin) checkpoint(t0 + tc - kChunk);
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
-                        hh[k][c][p] = fma2(exp2_2(mul2(uu[c], A2[c][p])), k ? hh[k ? k - 1 : 0][c][p] : h0[c][p], mul2(ux[c], Bp[p]));
+                        hh[k][c][p] = fma2(decay2(uu[c], A2[c][p]), k ? hh[k ? k - 1 : 0][c][p] : h0[c][p], mul2(ux[c], Bp[p]));
             }
 #pragma unroll
             for (int kb = kChunk - TB; kb >= 0; kb -= TB) {
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
                         f32x2 a1, a2;
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
-                            const f32x2 av = exp2_2(mul2(uu[c], A2[c][p]));
+                            const f32x2 av = decay2(uu[c], A2[c][p]);
                             dh[c][p] = fma2(Cp[p], gg[c], dh[c][p]);
                             vB[p] = c ? fma2(dh[c][p], ux[c], vB[p]) : mul2(dh[c][p], ux[c]);
                             vC[p] = c ? fma2(gg[c], hh[k][c][p], vC[p]) : mul2(gg[c], hh[k][c][p]);
@@ -333,8 +334,8 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
                     const float dd = fmaf(s2[0], kLn2, xs.x * s1[0]) * xs.y;
                     so[t * CPB + c0 + myc] = make_float2(fmaf(u, s1[0], Dsk * g), dd);
                     if (t0 + t < n) {
-                        dbs += dd;
-                        dDs = fmaf(g, xs.x, dDs);
+                        dbt += dd;
+                        dDt = fmaf(g, xs.x, dDt);
                     }
                 }
             }
@@ -342,6 +343,8 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) dA[c][p] = add2(dA[c][p], dAt[c][p]);
+            dbs += dbt;
+            dDs += dDt;
         }
         __syncthreads();
         // rows of dx and ddelta, and the CTA's share of dB and dC

@@ -24,81 +24,95 @@ constexpr int kSeqs = 4;
 template <typename T, int LN, int SPL, bool WIDE>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmArgs a, int per_group) {
     constexpr int CPB = kStepThreads / LN, Q = SPL / 4;
-    const int64_t nblk = (a.D + CPB - 1) / CPB;
-    const int64_t b0 = blockIdx.x / nblk * kSeqs;
+    const unsigned nblk = (a.D + CPB - 1) / CPB;
+    const int b0 = blockIdx.x / nblk * kSeqs;
     const int ln = threadIdx.x % LN, ch = threadIdx.x / LN, lane = threadIdx.x & 31;
     const int d = (int)(blockIdx.x % nblk) * CPB + ch, N = a.N;
     const bool live = d < a.D;
-    const int seqs = live ? (int)min((int64_t)kSeqs, a.B - b0) : 0;
-    const int grp = live ? d / per_group : 0;
+    const int seqs = live ? min(kSeqs, a.B - b0) : 0;
+    // the channel's place in the first sequence, and from one sequence to the next
+    const size_t to_tok = a.D, to_grp = (size_t)a.G * N, to_state = (size_t)a.D * N;
+    const size_t tok = live ? b0 * to_tok + d : 0, grp = live ? b0 * to_grp + (size_t)(d / per_group) * N : 0;
+    const T *xp = (const T *)a.x + tok, *dp = (const T *)a.delta + tok, *Bp = (const T *)a.Bm + grp, *Cp = (const T *)a.Cm + grp;
+    float *S = a.S_final + tok * N;
+    const float *A = a.A + (live ? (size_t)d * N : 0);
     const float bias = live && a.delta_bias ? a.delta_bias[d] : 0.f, skip = live && a.Dskip ? a.Dskip[d] : 0.f;
-    float u[kSeqs], x[kSeqs], acc[kSeqs];
-    float4 s[WIDE ? kSeqs : 1][Q];
+
+    ulonglong2 s[WIDE ? kSeqs : 1][Q];
     if constexpr (WIDE) {
 #pragma unroll
         for (int j = 0; j < kSeqs; ++j)
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
                 const int k = (i * LN + ln) * 4;
-                if (j < seqs && k < N) s[j][i] = *reinterpret_cast<const float4 *>(a.S_final + ((b0 + j) * a.D + d) * N + k);
+                if (j < seqs && k < N) s[j][i] = *reinterpret_cast<const ulonglong2 *>(S + j * to_state + k);
             }
     }
+    // a channel's lanes share out its sequences' inputs and hand them round
+    constexpr int MINE = (kSeqs + LN - 1) / LN;
+    float um[MINE + MINE % 2], xm[MINE], u[kSeqs], x[kSeqs], acc[kSeqs];
+    um[MINE - 1 + MINE % 2] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const size_t bd = (b0 + (j < seqs ? j : 0)) * a.D + (live ? d : 0);
-        x[j] = to_f(((const T *)a.x)[bd]);
-        u[j] = to_f(((const T *)a.delta)[bd]) + bias;
-        acc[j] = 0.f;
+    for (int i = 0; i < MINE; ++i) {
+        const int j = i * LN + ln;
+        xm[i] = j < seqs ? to_f(xp[j * to_tok]) : 0.f;
+        um[i] = j < seqs ? to_f(dp[j * to_tok]) + bias : 0.f;
     }
     if (a.softplus) {
         float e0, e1;
 #pragma unroll
-        for (int j = 0; j < kSeqs; j += 2) softplus2(u[j], u[j + 1], e0, e1);
+        for (int i = 0; i < MINE; i += 2) softplus2(um[i], um[i + 1], e0, e1);
+    }
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        x[j] = __shfl_sync(0xffffffffu, xm[j / LN], j % LN, LN);
+        u[j] = __shfl_sync(0xffffffffu, um[j / LN], j % LN, LN);
+        acc[j] = 0.f;
     }
     if constexpr (WIDE) {
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             const int k = (i * LN + ln) * 4;
             if (k >= N || !live) continue;
-            float4 A = *reinterpret_cast<const float4 *>(a.A + (size_t)d * N + k);
-            A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
+            const ulonglong2 Av = *reinterpret_cast<const ulonglong2 *>(A + k);
+            const f32x2 A2[2] = {mul2(Av.x, pk(kLog2e, kLog2e)), mul2(Av.y, pk(kLog2e, kLog2e))};
 #pragma unroll
             for (int j = 0; j < kSeqs; ++j) {
                 if (j >= seqs) continue;
-                const size_t at = ((b0 + j) * a.G + grp) * N + k;
                 Pack<T, 4> Bv, Cv;
-                float B[4], C[4];
-                Bv.load((const T *)a.Bm + at);
-                Cv.load((const T *)a.Cm + at);
-                Bv.get(B);
-                Cv.get(C);
-                const float ux = u[j] * x[j];
-                float4 &h = s[j][i];
-                h.x = fmaf(exp2_fast(u[j] * A.x), h.x, ux * B[0]);
-                h.y = fmaf(exp2_fast(u[j] * A.y), h.y, ux * B[1]);
-                h.z = fmaf(exp2_fast(u[j] * A.z), h.z, ux * B[2]);
-                h.w = fmaf(exp2_fast(u[j] * A.w), h.w, ux * B[3]);
-                acc[j] += h.x * C[0] + h.y * C[1] + h.z * C[2] + h.w * C[3];
-                *reinterpret_cast<float4 *>(a.S_final + ((b0 + j) * a.D + d) * N + k) = h;
+                f32x2 B[2], C[2];
+                Bv.load(Bp + j * to_grp + k);
+                Cv.load(Cp + j * to_grp + k);
+                Bv.get2(B);
+                Cv.get2(C);
+                const f32x2 uu = pk(u[j], u[j]), ux = pk(u[j] * x[j], u[j] * x[j]);
+                ulonglong2 &h = s[j][i];
+                h.x = fma2(decay2(uu, A2[0]), h.x, mul2(ux, B[0]));
+                h.y = fma2(decay2(uu, A2[1]), h.y, mul2(ux, B[1]));
+                acc[j] += sum2(fma2(h.x, C[0], mul2(h.y, C[1])));
+                *reinterpret_cast<ulonglong2 *>(S + j * to_state + k) = h;
             }
         }
     } else {
 #pragma unroll
         for (int j = 0; j < kSeqs; ++j) {
             if (j >= seqs) continue;
-            const T *Bp = (const T *)a.Bm + ((b0 + j) * a.G + grp) * N, *Cp = (const T *)a.Cm + ((b0 + j) * a.G + grp) * N;
-            float *S = a.S_final + ((b0 + j) * a.D + d) * N;
             for (int k = ln; k < N; k += LN) {
-                const float h = fmaf(exp2_fast(u[j] * (a.A[(size_t)d * N + k] * kLog2e)), S[k], u[j] * x[j] * to_f(Bp[k]));
-                acc[j] = fmaf(h, to_f(Cp[k]), acc[j]);
-                S[k] = h;
+                float &h = S[j * to_state + k];
+                h = fmaf(decay(u[j], A[k] * kLog2e), h, u[j] * x[j] * to_f(Bp[j * to_grp + k]));
+                acc[j] = fmaf(h, to_f(Cp[j * to_grp + k]), acc[j]);
             }
         }
     }
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        lane_reduce<1, LN, 1>(acc + j, lane);
-        if (j < seqs && ln == 0) ((T *)a.y)[(b0 + j) * a.D + d] = from_f<T>(fmaf(skip, x[j], acc[j]));
+    for (int j = 0; j < kSeqs; ++j) acc[j] += ln == 0 ? skip * x[j] : 0.f;
+    lane_reduce<kSeqs, LN, 1>(acc, lane);
+    const int first = reduced_first<kSeqs, LN, 1>(lane);
+    if (reduced_owner<kSeqs, LN, 1>(lane)) {
+        T *y = (T *)a.y + tok;
+#pragma unroll
+        for (int i = 0; i < (kSeqs > LN ? kSeqs / LN : 1); ++i)
+            if (first + i < seqs) y[(first + i) * to_tok] = from_f<T>(acc[i]);
     }
 }
 

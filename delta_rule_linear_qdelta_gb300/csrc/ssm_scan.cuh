@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                 const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(src + (bd + c) * NP + ln * 4);
                 const float U = s < 0 ? 0.f : w.U[s * all + bd + c];
                 const f32x2 UU = pk(U, U);
-                h[c][0] = fma2(exp2_2(mul2(UU, A2[c][0])), h[c][0], e.x);
-                h[c][1] = fma2(exp2_2(mul2(UU, A2[c][1])), h[c][1], e.y);
+                h[c][0] = fma2(decay2(UU, A2[c][0]), h[c][0], e.x);
+                h[c][1] = fma2(decay2(UU, A2[c][1]), h[c][1], e.y);
             }
         }
     }
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                         const float g = SEG ? sg[t * CPB + c0 + c] : 0.f;
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
-                            const f32x2 av = exp2_2(mul2(uu[c], A2[c][p]));
+                            const f32x2 av = decay2(uu[c], A2[c][p]);
                             h[c][p] = fma2(av, h[c][p], mul2(ux[c], Bv[p]));
                             if (OUT) acc = p ? fma2(Cv[p], h[c][p], acc) : mul2(Cv[p], h[c][p]);
                             if (SEG) {

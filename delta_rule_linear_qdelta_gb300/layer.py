@@ -20,9 +20,10 @@ def _arg(t, name, dtype, shape, dev, optional=False):
     """The address of an argument that is what it has to be; an error that says what is wrong
     otherwise.  One token's call spends most of its time on the host, so the usual case is a
     single test."""
-    if t is None and optional:
-        return None
-    if t is not None and t.device == dev and t.dtype == dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if t is None:
+        if optional:
+            return None
+    elif t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
         return t.data_ptr()
     _need(t, name, dtype, shape)
     _same_device(dev, t)
@@ -54,7 +55,7 @@ def _run(name, dev, stream, *args):
     """Calls the entry point `name` with `dev` current and the stream as its last argument."""
     fn = getattr(load_library(), name)
     st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream, dev)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         _check(fn(*args, st), name)
     else:
         with torch.cuda.device(dev):
@@ -86,7 +87,7 @@ def short_conv_step(S, x, w, bias=None, *, silu=True, y=None, stream=None):
     args = (_arg(S, "S", dt, (N, W - 1, D), dev), _arg(x, "x", dt, (N, D), dev), _arg(w, "w", F32, (D, W), dev),
             _arg(bias, "bias", F32, (D,), dev, True))
     code = _dtype_code(x)
-    y = _new(y, "y", dt, (N, D), dev)
+    y = torch.empty_like(x) if y is None else _new(y, "y", dt, (N, D), dev)
     _run("short_conv_step", dev, stream, *args, y.data_ptr(), N, D, W, int(silu), code)
     return y
 
