@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
     constexpr int VEC = St::VEC, PER = St::PER;
     extern __shared__ float4 smem4[];
     T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
-    float4 *su = smem4 + St::BYTES / 16;                                                // [kTile][PAIRS] (u0, u1, u0 x0, u1 x1)
-    float2 *sx = reinterpret_cast<float2 *>(su + kTile * PAIRS);       // [kTile][CPB] (x, softplus')
+    float4 *su = smem4 + St::BYTES / 16;                               // [kTile][pair_row] (u0, u1, u0 x0, u1 x1)
+    float2 *sx = reinterpret_cast<float2 *>(su + kTile * pair_row(PAIRS));  // [kTile][CPB] (x, softplus')
     float2 *so = sx + kTile * CPB;                                     // [kTile][CPB] (dx, ddelta)
     float2 *sg = so + kTile * CPB;                                     // [kTile][PAIRS] (g0, g1)
     float *sB = reinterpret_cast<float *>(sg + kTile * PAIRS);         // [4 orders][kTile][NP]
@@ -215,12 +215,12 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
             if constexpr (VEC == 4) {
 #pragma unroll
                 for (int k = 0; k < 4; k += 2) {
-                    su[t * PAIRS + (c + k) / 2] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
-                    sg[t * PAIRS + (c + k) / 2] = make_float2(g[k], g[k + 1]);
+                    su[t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS)] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
                     *reinterpret_cast<float4 *>(sx + t * CPB + c + k) = make_float4(x[k], sig[k], x[k + 1], sig[k + 1]);
                 }
+                *reinterpret_cast<float4 *>(sg + t * PAIRS + c / 2) = make_float4(g[0], g[1], g[2], g[3]);
             } else {
-                float *to = reinterpret_cast<float *>(su + t * PAIRS + c / 2) + (c & 1);
+                float *to = reinterpret_cast<float *>(su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS)) + (c & 1);
                 to[0] = u[0];
                 to[2] = u[0] * x[0];
                 reinterpret_cast<float *>(sg + t * PAIRS + c / 2)[c & 1] = g[0];
@@ -232,6 +232,8 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
             for (int o = 0; o < 4; ++o)
                 *reinterpret_cast<float4 *>((which ? sC : sB) + (o * kTile + t) * NP + k) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
         });
+        const float4 *mine = su + pair_at(pr, PAIRS);
+        const float *gB = sB + m * kTile * NP + ln * 4, *gC = sC + m * kTile * NP + ln * 4;
         __syncthreads();
 
 #pragma unroll 1
@@ -253,8 +255,8 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
 #pragma unroll
             for (int k = 0; k < kChunk; ++k) {
                 const int t = tc + k;
-                const float4 q = su[t * PAIRS + pr];
-                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(sB + (m * kTile + t) * NP + ln * 4);
+                const float4 q = mine[t * pair_row(PAIRS)];
+                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
                 const f32x2 Bp[2] = {Bv.x, Bv.y}, uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -268,10 +270,10 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
 #pragma unroll
                 for (int kk = TB - 1; kk >= 0; --kk) {
                     const int k = kb + kk, t = tc + k;
-                    const float4 q = su[t * PAIRS + pr];
+                    const float4 q = mine[t * pair_row(PAIRS)];
                     const float2 gv = sg[t * PAIRS + pr];
-                    const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(sB + (m * kTile + t) * NP + ln * 4);
-                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2 *>(sC + (m * kTile + t) * NP + ln * 4);
+                    const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
+                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2 *>(gC + t * NP);
                     const f32x2 Bp[2] = {Bv.x, Bv.y}, Cp[2] = {Cv.x, Cv.y};
                     const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
                     const f32x2 gg[2] = {pk(gv.x, gv.x), pk(gv.y, gv.y)};
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
                 lane_reduce<CNT, LN, 1>(s2, lane);
                 if (owner) {
                     const int t = tc + kb + myk;
-                    const float u = reinterpret_cast<const float *>(su + t * PAIRS + pr)[myc];
+                    const float u = reinterpret_cast<const float *>(mine + t * pair_row(PAIRS))[myc];
                     const float g = reinterpret_cast<const float *>(sg + t * PAIRS + pr)[myc];
                     const float2 xs = sx[t * CPB + c0 + myc];
                     const float dd = fmaf(s2[0], kLn2, xs.x * s1[0]) * xs.y;
@@ -417,7 +419,7 @@ template <typename T> __global__ void __launch_bounds__(kSumThreads) groups_kern
 
 template <typename T, int LN, bool WIDE> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
-    const size_t smem = Staging<T, kGradThreads, CPB, NP, 3, WIDE>::BYTES + kTile * (PAIRS * 4 + CPB * 4 + PAIRS * 2 + 2 * 4 * NP + kGradWarps * 2 * NP) * sizeof(float);
+    const size_t smem = Staging<T, kGradThreads, CPB, NP, 3, WIDE>::BYTES + kTile * (pair_row(PAIRS) * 4 + CPB * 4 + PAIRS * 2 + 8 * NP + kGradWarps * 2 * NP) * sizeof(float);
     const cudaError_t e = allow_smem(grads_kernel<T, LN, WIDE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));

@@ -11,7 +11,8 @@
 // LN lanes share a channel pair (4 LN = N rounded up).  Per token it reads 4 B, 4 C and two
 // (u, u x): 48 bytes for 8 states.  One channel by 4 states reads 40 bytes for 4 and is bound by
 // the shared-memory pipe; 2 by 8 reads less per state but needs as many instructions and halves
-// the warps, which the recurrence needs to cover its latencies.
+// the warps, which the recurrence needs to cover its latencies.  (bf16 B and C kept as they come
+// halve the reads, but unpacking them at every use costs more: 557 -> 602 us, 32768 tokens.)
 // A CTA of four warps takes CPB = 256 / LN channels of one sequence and walks its tokens in tiles
 // of 16, staged in shared memory as fp32 (softplus once per token and channel) while the next
 // two tiles are on their way.  y goes back through shared memory, so rows are written as they
@@ -66,6 +67,11 @@ template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
 }
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int T) { return lens ? min(max(lens[b], 0), T) : T; }
+
+// Where a token's channel pair p lies in a row of staged pairs: even and odd ones apart, so that a
+// thread's two neighbouring pairs are written, and a warp's read, without bank conflicts.
+__host__ __device__ constexpr int pair_at(int p, int PAIRS) { return p / 2 + (p & 1) * (PAIRS / 2 + 4); }
+__host__ __device__ constexpr int pair_row(int PAIRS) { return PAIRS + 4; }
 
 // u = softplus(delta + bias), or the sum, of VEC channels.
 template <int VEC> __device__ __forceinline__ void step_sizes(float (&u)[VEC], const float (&bias)[VEC], int softplus) {
@@ -156,7 +162,8 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
         }
         v.get(f);
     }
-    // put(which, t, k, f): B (0) or C (1) of token t, states k .. k + 3
+    // put(which, t, k, f) for the four states from k of token t that this thread has copied (or, odd
+    // shapes, reads now): for the CTA to lay B and C out in its own way.
     template <typename F>
     __device__ __forceinline__ static void get_groups(const T *raw, int buf, const SsmArgs &a, const ChannelBlock &cb, int b, int t0,
                                                       int n, bool both, F put) {
@@ -209,8 +216,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
     constexpr int VEC = St::VEC, PER = St::PER;
     extern __shared__ float4 smem4[];
     T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
-    float4 *su = smem4 + St::BYTES / 16;                               // [kTile][PAIRS] (u0, u1, u0 x0, u1 x1)
-    float *sB = reinterpret_cast<float *>(su + kTile * PAIRS);         // [kTile][NP]
+    float4 *su = smem4 + St::BYTES / 16;                               // [kTile][pair_row] (u0, u1, u0 x0, u1 x1)
+    float *sB = reinterpret_cast<float *>(su + kTile * pair_row(PAIRS));  // [kTile][NP]
     float *sC = sB + kTile * NP;                                       // [kTile][NP]         BOTH
     float *sy = sC + kTile * NP;                                       // [kTile][YS] y       OUT
     float *sg = sy;                                                    // [kTile][CPB] dy     SEG
@@ -300,9 +307,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
             if constexpr (VEC == 4) {
 #pragma unroll
                 for (int k = 0; k < 4; k += 2)
-                    su[t * PAIRS + (c + k) / 2] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
+                    su[t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS)] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
             } else {
-                float *to = reinterpret_cast<float *>(su + t * PAIRS + c / 2) + (c & 1);
+                float *to = reinterpret_cast<float *>(su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS)) + (c & 1);
                 to[0] = u[0];
                 to[2] = u[0] * x[0];
             }
@@ -316,6 +323,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         St::get_groups(raw, buf, a, cb, b, t0, n, BOTH, [&](int which, int t, int k, const float (&f)[4]) {
             *reinterpret_cast<float4 *>((which ? sC : sB) + t * NP + k) = make_float4(f[0], f[1], f[2], f[3]);
         });
+        const float4 *mine = su + pair_at(pr, PAIRS);
         __syncthreads();
 #pragma unroll 1
         for (int tc = 0; tc < kTile; tc += kChunk) {
@@ -330,14 +338,14 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                     if (c0 + 1 < cb.count) w.ucum[row + 1] = u1;
                 }
             }
-            constexpr int UNROLL = TB >= 4 ? 1 : 4 / TB;
+            constexpr int UNROLL = kChunk / TB;
 #pragma unroll UNROLL
             for (int tb = 0; tb < kChunk; tb += TB) {
                 float v[CNT];
 #pragma unroll
                 for (int k = 0; k < TB; ++k) {
                     const int t = tc + tb + k;
-                    const float4 q = su[t * PAIRS + pr];
+                    const float4 q = mine[t * pair_row(PAIRS)];
                     const ulonglong2 Bq = *reinterpret_cast<const ulonglong2 *>(sB + t * NP + ln * 4);
                     const ulonglong2 Cq = BOTH ? *reinterpret_cast<const ulonglong2 *>(sC + t * NP + ln * 4) : ulonglong2{};
                     const f32x2 Bv[2] = {Bq.x, Bq.y}, Cv[2] = {Cq.x, Cq.y};
@@ -432,8 +440,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
 template <typename T, int LN, bool WIDE, int MODE>
 cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
     constexpr int CPB = 2 * kScanThreads / LN, NP = 4 * LN, YS = scan_row(LN);
-    const size_t raw = Staging<T, kScanThreads, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, WIDE>::BYTES;
-    const size_t smem = raw + (kTile * 2 * CPB + 2 * kTile * NP + kTile * YS) * sizeof(float);
+    using St = Staging<T, kScanThreads, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, WIDE>;
+    const size_t smem = St::BYTES + kTile * (4 * pair_row(CPB / 2) + 2 * NP + YS) * sizeof(float);
     const cudaError_t e = allow_smem(scan_kernel<T, LN, WIDE, MODE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
