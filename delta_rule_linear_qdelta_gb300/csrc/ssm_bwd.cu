@@ -19,8 +19,6 @@
 //     and segments; in a fixed order, so results do not change from run to run.
 // Bound by instruction issue and the shared-memory pipe: two exponentials and about 20
 // operations per (token, channel, state) in launch 2, one and 4 in launch 1.
-#include <limits.h>
-
 #include "layer_common.cuh"
 #include "ssm_scan.cuh"
 
@@ -165,10 +163,9 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
     float bias[VEC];
     if (St::FIXED) St::param(a.delta_bias, cb, 0, bias);
     const int tiles = t_begin < t_end ? (t_end - t_begin + kTile - 1) / kTile : 0;
+    typename St::Cursor at(a, cb, b, t_begin + (tiles - 1) * kTile, {a.x, a.delta, a.dy});
     // the tile-th tile of the segment, none (and no copies) before the first
-    auto issue = [&](int tile, int buf) {
-        St::issue(raw, buf, a, cb, b, t_begin + tile * kTile, tile >= 0 ? t_end : INT_MIN, n, true, {a.x, a.delta, a.dy});
-    };
+    auto issue = [&](int tile, int buf) { St::issue(at, raw, buf, a, cb, t_begin + tile * kTile, tile >= 0, n, true, -1); };
     issue(tiles - 1, 0);
     issue(tiles - 2, 1);
     // the checkpoint of the next chunk is on its way while one is computed
@@ -350,23 +347,32 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
         }
         __syncthreads();
         // rows of dx and ddelta, and the CTA's share of dB and dC
+        const size_t out = ((size_t)b * a.T + t0 + St::tok(0)) * D + cb.first + St::chan(0);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int t = St::tok(i), c = St::chan(i);
-            if (t >= kTile || t0 + t >= t_stop || c >= cb.count) continue;
+            if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
+            if ((PER * kGradThreads != kTile * St::ROW || !WIDE) && t >= kTile) continue;
             float fx[VEC], fd[VEC];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const float2 o = so[t * CPB + c + k];
-                fx[k] = t0 + t < n ? o.x : 0.f;
-                fd[k] = t0 + t < n ? o.y : 0.f;
+            if constexpr (VEC == 4) {
+                const float4 o0 = *reinterpret_cast<const float4 *>(so + t * CPB + c), o1 = *reinterpret_cast<const float4 *>(so + t * CPB + c + 2);
+                fx[0] = o0.x; fd[0] = o0.y; fx[1] = o0.z; fd[1] = o0.w;
+                fx[2] = o1.x; fd[2] = o1.y; fx[3] = o1.z; fd[3] = o1.w;
+            } else {
+                const float2 o = so[t * CPB + c];
+                fx[0] = o.x;
+                fd[0] = o.y;
             }
-            const size_t at = ((size_t)b * a.T + t0 + t) * D + cb.first + c;
+            if (!full && t0 + t >= n) {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) fx[k] = fd[k] = 0.f;
+            }
+            const size_t to = WIDE ? out + i * at.rows : ((size_t)b * a.T + t0 + t) * D + cb.first + c;
             typename St::Vec v;
             v.set(fx);
-            v.store((T *)a.dx + at);
+            v.store((T *)a.dx + to);
             v.set(fd);
-            v.store((T *)a.ddelta + at);
+            v.store((T *)a.ddelta + to);
         }
         for (int e = tid; e < kTile * 2 * NP; e += kGradThreads) {
             const int t = e / (2 * NP), k = e % (2 * NP);

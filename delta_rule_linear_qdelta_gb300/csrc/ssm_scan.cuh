@@ -119,32 +119,65 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
     }
     // Whether the whole tile at t0 is real: no padding, no channels beyond the block's.
     __device__ __forceinline__ static bool full(const ChannelBlock &cb, int t0, int n) { return t0 + kTile <= n && cb.count == CPB; }
-    // Starts the copies of the tile at t0 into buffer `buf` (one group of copies, possibly empty).
-    __device__ __forceinline__ static void issue(T *raw, int buf, const SsmArgs &a, const ChannelBlock &cb, int b, int t0, int end,
-                                                 int n, bool both, const void *const (&src)[NA]) {
-        if constexpr (WIDE) {
-            static_assert(FIXED);
-            T *to = raw + (size_t)buf * STAGE;
-            if (t0 < end) {
-                const bool all = full(cb, t0, n);
-                const size_t base = (size_t)b * a.T * a.D + cb.first + chan(0);
+    // A thread's place in the arrays, moved from tile to tile: addresses are worked out once.
+    struct Cursor {
+        const T *p[NA], *g[GPER];
+        size_t rows;                                                   // from one access of a tile to the next
+        __device__ __forceinline__ Cursor(const SsmArgs &a, const ChannelBlock &cb, int b, int t0, const void *const (&src)[NA]) {
+            rows = (size_t)(THREADS / ROW) * a.D;
+            if constexpr (WIDE) {
+                static_assert(FIXED);
+                const ptrdiff_t at = ((ptrdiff_t)b * a.T + t0 + tok(0)) * a.D + cb.first + chan(0);
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    if (tok(i) >= kTile) break;
-                    const bool on = all || (t0 + tok(i) < n && chan(0) < cb.count);
-                    const size_t at = on ? base + (size_t)(t0 + tok(i)) * a.D : 0;
-#pragma unroll
-                    for (int j = 0; j < NA; ++j)
-                        copy_async<4 * sizeof(T)>(to + j * kTile * CPB + (threadIdx.x + i * THREADS) * 4, (const T *)src[j] + at, on);
-                }
+                for (int j = 0; j < NA; ++j) p[j] = (const T *)src[j] + at;
 #pragma unroll
                 for (int i = 0; i < GPER; ++i) {
                     const int e = threadIdx.x + i * THREADS, which = e / (kTile * GROW), r = e % (kTile * GROW);
-                    const int t = r / GROW, k = r % GROW * 4;
-                    if (e >= (both ? GALL : GALL / 2)) break;
-                    const bool on = t0 + t < n && k < a.N;
-                    copy_async<4 * sizeof(T)>(to + NA * kTile * CPB + e * 4, groups(a, cb, b, on ? t0 + t : 0, which) + (on ? k : 0), on);
+                    g[i] = (const T *)(which ? a.Cm : a.Bm) + (((ptrdiff_t)b * a.T + t0 + r / GROW) * a.G + cb.group) * a.N + r % GROW * 4;
                 }
+            }
+        }
+        __device__ __forceinline__ void move(const SsmArgs &a, int tiles) {
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int j = 0; j < NA; ++j) p[j] += (ptrdiff_t)tiles * kTile * a.D;
+#pragma unroll
+                for (int i = 0; i < GPER; ++i) g[i] += (ptrdiff_t)tiles * kTile * a.G * a.N;
+            }
+        }
+    };
+    // Starts the copies of the cursor's tile, which is at t0, into buffer `buf` (one group of copies,
+    // empty where `any` is false) and moves the cursor by `step` tiles.
+    __device__ __forceinline__ static void issue(Cursor &at, T *raw, int buf, const SsmArgs &a, const ChannelBlock &cb, int t0, bool any,
+                                                 int n, bool both, int step) {
+        if constexpr (WIDE) {
+            T *to = raw + (size_t)buf * STAGE + threadIdx.x * 4;
+            if (any) {
+                if (full(cb, t0, n)) {
+#pragma unroll
+                    for (int j = 0; j < NA; ++j) {
+#pragma unroll
+                        for (int i = 0; i < PER; ++i)
+                            if (PER * THREADS == kTile * ROW || tok(i) < kTile)
+                                copy_async<4 * sizeof(T)>(to + j * kTile * CPB + i * THREADS * 4, at.p[j] + i * at.rows);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        if (tok(i) >= kTile) break;
+                        const bool on = t0 + tok(i) < n && chan(0) < cb.count;
+#pragma unroll
+                        for (int j = 0; j < NA; ++j)
+                            copy_async<4 * sizeof(T)>(to + j * kTile * CPB + i * THREADS * 4, on ? at.p[j] + i * at.rows : at.p[j], on);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < GPER; ++i) {
+                    const int e = threadIdx.x + i * THREADS, r = e % (kTile * GROW);
+                    if (e < (both ? GALL : GALL / 2))
+                        copy_async<4 * sizeof(T)>(to + NA * kTile * CPB + i * THREADS * 4, at.g[i], t0 + r / GROW < n && r % GROW * 4 < a.N);
+                }
+                at.move(a, step);
             }
             copies_issued();
         }
@@ -279,10 +312,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         St::param(a.delta_bias, cb, 0, bias);
         if (OUT) St::param(a.Dskip, cb, 0, skip);
     }
-    auto issue = [&](int t0, int buf) {
-        if constexpr (SEG) St::issue(raw, buf, a, cb, b, t0, t_end, n, BOTH, {a.x, a.delta, a.dy});
-        else St::issue(raw, buf, a, cb, b, t0, t_end, n, BOTH, {a.x, a.delta});
+    auto cursor = [&] {
+        if constexpr (SEG) return typename St::Cursor(a, cb, b, t_begin, {a.x, a.delta, a.dy});
+        else return typename St::Cursor(a, cb, b, t_begin, {a.x, a.delta});
     };
+    typename St::Cursor at = cursor();
+    auto issue = [&](int t0, int buf) { St::issue(at, raw, buf, a, cb, t0, t0 < t_end, n, BOTH, 1); };
+    T *y = OUT ? (T *)a.y + ((size_t)b * a.T + t_begin + St::tok(0)) * D + cb.first + St::chan(0) : nullptr;
     f32x2 U = 0;                                                       // of the two channels
     issue(t_begin, 0);
     issue(t_begin + kTile, 1);
@@ -380,7 +416,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int t = St::tok(i), c = St::chan(i);
-                if (t >= kTile || t0 + t >= t_stop || c >= cb.count) continue;
+                if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
+                if ((PER * kScanThreads != kTile * St::ROW || !WIDE) && t >= kTile) continue;
                 if (!St::FIXED) St::param(a.Dskip, cb, i, skip);
                 float f[VEC], x[VEC];
                 St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
@@ -390,15 +427,20 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                 } else {
                     f[0] = sy[t * YS + c];
                 }
+                if (a.Dskip) {
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    if (a.Dskip) f[k] = fmaf(skip[k], x[k], f[k]);
-                    if (!full && t0 + t >= n) f[k] = 0.f;
+                    for (int k = 0; k < VEC; ++k) f[k] = fmaf(skip[k], x[k], f[k]);
+                }
+                if (!full && t0 + t >= n) {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) f[k] = 0.f;
                 }
                 typename St::Vec o;
                 o.set(f);
-                o.store((T *)a.y + ((size_t)b * a.T + t0 + t) * D + cb.first + c);
+                if constexpr (WIDE) o.store(y + i * at.rows);
+                else o.store((T *)a.y + ((size_t)b * a.T + t0 + t) * D + cb.first + c);
             }
+            y += (size_t)kTile * D;
         }
     }
     if constexpr (OUT) {                                               // whole tiles of padding
