@@ -68,22 +68,26 @@ BwdWs bwd_ws(int B, int T, int D, int G, int N) {
 // pairs make a warp.  dB and dC of a token are sums over the warp's channels of 4 states each:
 // they are joined like lane_reduce, but a lane keeps its four states in the order n ^ m, m two
 // of its channel bits, so what it gives away is always its upper half and nothing has to be
-// selected; B and C lie in shared memory in all four orders.
+// selected; B and C lie in shared memory in all four orders.  The sums over n behind dx and
+// ddelta are left as parts in shared memory for the thread that writes the rows.
+// Row of the parts: float4 (s1 of both channels, s2 of both), free of bank conflicts.
+__host__ __device__ constexpr int part_row(int LN) { return kGradThreads / LN + (LN == 2 ? 4 : 2); }
+
 template <typename T, int LN, bool WIDE>
-__global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
+__global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN, CL = 32 / LN;
-    constexpr int TB = LN >= 4 ? 2 : 1, CNT = 2 * TB;                  // tokens whose sums over n join at once
-    using St = Staging<T, kGradThreads, CPB, NP, 3, WIDE>;
+    constexpr int PARTS = sum_parts(LN), NL = LN / PARTS, PR = part_row(LN);
+    using St = Staging<T, kGradThreads, kChunk, CPB, NP, 3, WIDE>;
     constexpr int VEC = St::VEC, PER = St::PER;
     extern __shared__ float4 smem4[];
-    T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
-    float4 *su = smem4 + St::BYTES / 16;                               // [kTile][pair_row] (u0, u1, u0 x0, u1 x1)
-    float2 *sx = reinterpret_cast<float2 *>(su + kTile * pair_row(PAIRS));  // [kTile][CPB] (x, softplus')
-    float2 *so = sx + kTile * CPB;                                     // [kTile][CPB] (dx, ddelta)
-    float2 *sg = so + kTile * CPB;                                     // [kTile][PAIRS] (g0, g1)
-    float *sB = reinterpret_cast<float *>(sg + kTile * PAIRS);         // [4 orders][kTile][NP]
-    float *sC = sB + 4 * kTile * NP;
-    float *sr = sC + 4 * kTile * NP;                                   // [warps][kTile][2 NP] (dB, dC)
+    T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] chunks on their way
+    float4 *su = smem4 + St::BYTES / 16;                               // [kChunk][pair_row] (u0, u1, u0 x0, u1 x1)
+    float4 *sp = su + kChunk * pair_row(PAIRS);                        // [kChunk][PARTS][PR] parts of the sums over n
+    float2 *sg = reinterpret_cast<float2 *>(sp + kChunk * PARTS * PR); // [kChunk][PAIRS] (g0, g1)
+    float *ss = reinterpret_cast<float *>(sg + kChunk * PAIRS);        // [kChunk][CPB] softplus'
+    float *sB = ss + kChunk * CPB;                                     // [4 orders][kChunk][NP]
+    float *sC = sB + 4 * kChunk * NP;
+    float *sr = sC + 4 * kChunk * NP;                                  // [warps][kChunk][2 NP] (dB, dC)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = tid % LN, pr = tid / LN, seg = blockIdx.y;
     const int cl = lane / LN, m = (CL >= 2 ? (cl & 1) * 2 : 0) + (CL >= 4 ? cl >> 1 & 1 : 0);
@@ -154,20 +158,17 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
             }
         }
     }
-    // the (token, channel) of a batch whose sums over n this lane ends up with
-    const int mine = reduced_first<CNT, LN, 1>(lane), myk = mine / 2, myc = mine & 1;
-    const bool owner = reduced_owner<CNT, LN, 1>(lane);
-    const float Dsk = a.Dskip && c0 + myc < cb.count ? a.Dskip[cb.first + c0 + myc] : 0.f;
-    float dDs = 0.f, dbs = 0.f;
-
-    float bias[VEC];
-    if (St::FIXED) St::param(a.delta_bias, cb, 0, bias);
-    const int tiles = t_begin < t_end ? (t_end - t_begin + kTile - 1) / kTile : 0;
-    typename St::Cursor at(a, cb, b, t_begin + (tiles - 1) * kTile, {a.x, a.delta, a.dy});
-    // the tile-th tile of the segment, none (and no copies) before the first
-    auto issue = [&](int tile, int buf) { St::issue(at, raw, buf, a, cb, t_begin + tile * kTile, tile >= 0, n, true, -1); };
-    issue(tiles - 1, 0);
-    issue(tiles - 2, 1);
+    float bias[VEC], skip[VEC], dDs[VEC], dbs[VEC];                    // of the channels this thread writes
+    St::param(a.delta_bias, cb, bias);
+    St::param(a.Dskip, cb, skip);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) dDs[k] = dbs[k] = 0.f;
+    const int chunks = t_begin < t_end ? (t_end - t_begin + kChunk - 1) / kChunk : 0;
+    typename St::Cursor at(a, cb, b, t_begin + (chunks - 1) * kChunk, {a.x, a.delta, a.dy});
+    // the c-th chunk of the segment, none (and no copies) before the first
+    auto issue = [&](int c, int buf) { St::issue(at, raw, buf, a, cb, t_begin + c * kChunk, c >= 0, n, true, -1); };
+    issue(chunks - 1, 0);
+    issue(chunks - 2, 1);
     // the checkpoint of the next chunk is on its way while one is computed
     float4 ck_h[2];
     float ck_u[2];
@@ -179,19 +180,18 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
             if (S > 1) ck_u[c] = ws[w.ucum + row];
         }
     };
-    if (tiles) checkpoint(t_begin + (t_end - 1 - t_begin) / kChunk * kChunk);
+    if (chunks) checkpoint(t_begin + (chunks - 1) * kChunk);
     int buf = 0;
-    for (int tile = tiles - 1; tile >= 0; --tile, buf = buf + 1 < kStages ? buf + 1 : 0) {
-        const int t0 = t_begin + tile * kTile;
-        issue(tile - 2, buf + 2 < kStages ? buf + 2 : buf + 2 - kStages);
+    for (int chunk = chunks - 1; chunk >= 0; --chunk, buf = buf + 1 < kStages ? buf + 1 : 0) {
+        const int t0 = t_begin + chunk * kChunk;
+        issue(chunk - 2, buf + 2 < kStages ? buf + 2 : buf + 2 - kStages);
         if constexpr (WIDE) copies_done<2>();
         const bool full = St::full(cb, t0, n);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = St::tok(i), c = St::chan(i);
-            if (t >= kTile) break;
+            const int t = St::tok(i), c = St::chan();
+            if (t >= kChunk) break;
             float u[VEC], x[VEC], g[VEC], sig[VEC];
-            if (!St::FIXED) St::param(a.delta_bias, cb, i, bias);
             St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
             St::get(raw, buf, 1, i, a, cb, b, t0, n, a.delta, u);
             St::get(raw, buf, 2, i, a, cb, b, t0, n, a.dy, g);
@@ -211,161 +211,154 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
             }
             if constexpr (VEC == 4) {
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
+                for (int k = 0; k < 4; k += 2)
                     su[t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS)] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
-                    *reinterpret_cast<float4 *>(sx + t * CPB + c + k) = make_float4(x[k], sig[k], x[k + 1], sig[k + 1]);
-                }
+                *reinterpret_cast<float4 *>(ss + t * CPB + c) = make_float4(sig[0], sig[1], sig[2], sig[3]);
                 *reinterpret_cast<float4 *>(sg + t * PAIRS + c / 2) = make_float4(g[0], g[1], g[2], g[3]);
             } else {
                 float *to = reinterpret_cast<float *>(su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS)) + (c & 1);
                 to[0] = u[0];
                 to[2] = u[0] * x[0];
                 reinterpret_cast<float *>(sg + t * PAIRS + c / 2)[c & 1] = g[0];
-                sx[t * CPB + c] = make_float2(x[0], sig[0]);
+                ss[t * CPB + c] = sig[0];
             }
         }
         St::get_groups(raw, buf, a, cb, b, t0, n, true, [&](int which, int t, int k, const float (&f)[4]) {
 #pragma unroll
             for (int o = 0; o < 4; ++o)
-                *reinterpret_cast<float4 *>((which ? sC : sB) + (o * kTile + t) * NP + k) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
+                *reinterpret_cast<float4 *>((which ? sC : sB) + (o * kChunk + t) * NP + k) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
         });
         const float4 *mine = su + pair_at(pr, PAIRS);
-        const float *gB = sB + m * kTile * NP + ln * 4, *gC = sC + m * kTile * NP + ln * 4;
+        const float *gB = sB + m * kChunk * NP + ln * 4, *gC = sC + m * kChunk * NP + ln * 4;
         __syncthreads();
 
-#pragma unroll 1
-        for (int tc = kTile - kChunk; tc >= 0; tc -= kChunk) {
-            if (t0 + tc >= t_end) continue;                            // uniform over the CTA
-            f32x2 h0[2][2], hh[kChunk][2][2], dAt[2][2] = {};
-            float dbt = 0.f, dDt = 0.f;                                // a chunk's share: short sums lose less
+        f32x2 h0[2][2], hh[kChunk][2][2], dAt[2][2] = {};              // dAt: the chunk's share; short sums lose less
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const bool on = c0 + c < cb.count;
-                order(on ? ck_h[c] : make_float4(0.f, 0.f, 0.f, 0.f), h0[c]);
-                if (seg > 0) {
-                    const float U = on ? ck_u[c] : 0.f;
+        for (int c = 0; c < 2; ++c) {
+            const bool on = c0 + c < cb.count;
+            order(on ? ck_h[c] : make_float4(0.f, 0.f, 0.f, 0.f), h0[c]);
+            if (seg > 0) {
+                const float U = on ? ck_u[c] : 0.f;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) h0[c][p] = fma2(decay2(pk(U, U), A2[c][p]), hin[c][p], h0[c][p]);
-                }
+                for (int p = 0; p < 2; ++p) h0[c][p] = fma2(decay2(pk(U, U), A2[c][p]), hin[c][p], h0[c][p]);
             }
-            if (t0 + tc > t_begin) checkpoint(t0 + tc - kChunk);
+        }
+        if (chunk > 0) checkpoint(t0 - kChunk);
 #pragma unroll
-            for (int k = 0; k < kChunk; ++k) {
-                const int t = tc + k;
-                const float4 q = mine[t * pair_row(PAIRS)];
-                const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
-                const f32x2 Bp[2] = {Bv.x, Bv.y}, uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        hh[k][c][p] = fma2(decay2(uu[c], A2[c][p]), k ? hh[k ? k - 1 : 0][c][p] : h0[c][p], mul2(ux[c], Bp[p]));
-            }
-#pragma unroll
-            for (int kb = kChunk - TB; kb >= 0; kb -= TB) {
-                float s1[CNT], s2[CNT];
-#pragma unroll
-                for (int kk = TB - 1; kk >= 0; --kk) {
-                    const int k = kb + kk, t = tc + k;
-                    const float4 q = mine[t * pair_row(PAIRS)];
-                    const float2 gv = sg[t * PAIRS + pr];
-                    const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
-                    const ulonglong2 Cv = *reinterpret_cast<const ulonglong2 *>(gC + t * NP);
-                    const f32x2 Bp[2] = {Bv.x, Bv.y}, Cp[2] = {Cv.x, Cv.y};
-                    const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
-                    const f32x2 gg[2] = {pk(gv.x, gv.x), pk(gv.y, gv.y)};
-                    f32x2 vB[2], vC[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        f32x2 a1, a2;
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const f32x2 av = decay2(uu[c], A2[c][p]);
-                            dh[c][p] = fma2(Cp[p], gg[c], dh[c][p]);
-                            vB[p] = c ? fma2(dh[c][p], ux[c], vB[p]) : mul2(dh[c][p], ux[c]);
-                            vC[p] = c ? fma2(gg[c], hh[k][c][p], vC[p]) : mul2(gg[c], hh[k][c][p]);
-                            a1 = p ? fma2(dh[c][p], Bp[p], a1) : mul2(dh[c][p], Bp[p]);
-                            dh[c][p] = mul2(dh[c][p], av);             // a dh: what reaches h_{t-1}
-                            const f32x2 r = mul2(dh[c][p], k ? hh[k ? k - 1 : 0][c][p] : h0[c][p]);
-                            a2 = p ? fma2(A2[c][p], r, a2) : mul2(A2[c][p], r);
-                            dAt[c][p] = fma2(uu[c], r, dAt[c][p]);
-                        }
-                        s1[2 * kk + c] = sum2(a1);
-                        s2[2 * kk + c] = sum2(a2);
-                    }
-                    // dB, dC over the warp's channels: states 0, 1 of the lane's order are kept, then
-                    // state 0, then one of dB and dC
-                    if constexpr (CL >= 2) {
-                        vB[0] = add2(vB[0], __shfl_xor_sync(0xffffffffu, vB[1], LN));
-                        vC[0] = add2(vC[0], __shfl_xor_sync(0xffffffffu, vC[1], LN));
-                    }
-                    float *to = sr + (warp * kTile + t) * 2 * NP + ln * 4;
-                    float bl, bh, cl0, ch;
-                    unpk(vB[0], bl, bh);
-                    unpk(vC[0], cl0, ch);
-                    if constexpr (CL >= 4) {
-                        bl += __shfl_xor_sync(0xffffffffu, bh, 2 * LN);
-                        cl0 += __shfl_xor_sync(0xffffffffu, ch, 2 * LN);
-                    }
-                    if constexpr (CL >= 8) {
-                        const bool wc = cl & 4;
-                        float r = (wc ? cl0 : bl) + __shfl_xor_sync(0xffffffffu, wc ? bl : cl0, 4 * LN);
-                        if constexpr (CL >= 16) r += __shfl_xor_sync(0xffffffffu, r, 8 * LN);
-                        if (CL < 16 || !(cl & 8)) to[(wc ? NP : 0) + m] = r;
-                    } else if constexpr (CL == 4) {
-                        to[m] = bl;
-                        to[NP + m] = cl0;
-                    } else if constexpr (CL == 2) {
-                        *reinterpret_cast<float2 *>(to + m) = make_float2(bl, bh);
-                        *reinterpret_cast<float2 *>(to + NP + m) = make_float2(cl0, ch);
-                    } else {
-                        *reinterpret_cast<ulonglong2 *>(to) = make_ulonglong2(vB[0], vB[1]);
-                        *reinterpret_cast<ulonglong2 *>(to + NP) = make_ulonglong2(vC[0], vC[1]);
-                    }
-                }
-                lane_reduce<CNT, LN, 1>(s1, lane);
-                lane_reduce<CNT, LN, 1>(s2, lane);
-                if (owner) {
-                    const int t = tc + kb + myk;
-                    const float u = reinterpret_cast<const float *>(mine + t * pair_row(PAIRS))[myc];
-                    const float g = reinterpret_cast<const float *>(sg + t * PAIRS + pr)[myc];
-                    const float2 xs = sx[t * CPB + c0 + myc];
-                    const float dd = fmaf(s2[0], kLn2, xs.x * s1[0]) * xs.y;
-                    so[t * CPB + c0 + myc] = make_float2(fmaf(u, s1[0], Dsk * g), dd);
-                    if (t0 + t < n) {
-                        dbt += dd;
-                        dDt = fmaf(g, xs.x, dDt);
-                    }
-                }
-            }
+        for (int k = 0; k < kChunk; ++k) {
+            const float4 q = mine[k * pair_row(PAIRS)];
+            const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(gB + k * NP);
+            const f32x2 Bp[2] = {Bv.x, Bv.y}, uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int p = 0; p < 2; ++p) dA[c][p] = add2(dA[c][p], dAt[c][p]);
-            dbs += dbt;
-            dDs += dDt;
+                for (int p = 0; p < 2; ++p)
+                    hh[k][c][p] = fma2(decay2(uu[c], A2[c][p]), k ? hh[k ? k - 1 : 0][c][p] : h0[c][p], mul2(ux[c], Bp[p]));
         }
+#pragma unroll
+        for (int t = kChunk - 1; t >= 0; --t) {
+            const float4 q = mine[t * pair_row(PAIRS)];
+            const float2 gv = sg[t * PAIRS + pr];
+            const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
+            const ulonglong2 Cv = *reinterpret_cast<const ulonglong2 *>(gC + t * NP);
+            const f32x2 Bp[2] = {Bv.x, Bv.y}, Cp[2] = {Cv.x, Cv.y};
+            const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
+            const f32x2 gg[2] = {pk(gv.x, gv.x), pk(gv.y, gv.y)};
+            f32x2 vB[2], vC[2];
+            float v[4];                                                // sums over n: dh B of both channels, A r of both
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f32x2 a1, a2;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const f32x2 av = decay2(uu[c], A2[c][p]);
+                    dh[c][p] = fma2(Cp[p], gg[c], dh[c][p]);
+                    vB[p] = c ? fma2(dh[c][p], ux[c], vB[p]) : mul2(dh[c][p], ux[c]);
+                    vC[p] = c ? fma2(gg[c], hh[t][c][p], vC[p]) : mul2(gg[c], hh[t][c][p]);
+                    a1 = p ? fma2(dh[c][p], Bp[p], a1) : mul2(dh[c][p], Bp[p]);
+                    dh[c][p] = mul2(dh[c][p], av);             // a dh: what reaches h_{t-1}
+                    const f32x2 r = mul2(dh[c][p], t ? hh[t ? t - 1 : 0][c][p] : h0[c][p]);
+                    a2 = p ? fma2(A2[c][p], r, a2) : mul2(A2[c][p], r);
+                    dAt[c][p] = fma2(uu[c], r, dAt[c][p]);
+                }
+                v[c] = sum2(a1);
+                v[2 + c] = sum2(a2);
+            }
+            // dB, dC over the warp's channels: states 0, 1 of the lane's order are kept, then
+            // state 0, then one of dB and dC
+            if constexpr (CL >= 2) {
+                vB[0] = add2(vB[0], __shfl_xor_sync(0xffffffffu, vB[1], LN));
+                vC[0] = add2(vC[0], __shfl_xor_sync(0xffffffffu, vC[1], LN));
+            }
+            float *to = sr + (warp * kChunk + t) * 2 * NP + ln * 4;
+            float bl, bh, cl0, ch;
+            unpk(vB[0], bl, bh);
+            unpk(vC[0], cl0, ch);
+            if constexpr (CL >= 4) {
+                bl += __shfl_xor_sync(0xffffffffu, bh, 2 * LN);
+                cl0 += __shfl_xor_sync(0xffffffffu, ch, 2 * LN);
+            }
+            if constexpr (CL >= 8) {
+                const bool wc = cl & 4;
+                float r = (wc ? cl0 : bl) + __shfl_xor_sync(0xffffffffu, wc ? bl : cl0, 4 * LN);
+                if constexpr (CL >= 16) r += __shfl_xor_sync(0xffffffffu, r, 8 * LN);
+                if (CL < 16 || !(cl & 8)) to[(wc ? NP : 0) + m] = r;
+            } else if constexpr (CL == 4) {
+                to[m] = bl;
+                to[NP + m] = cl0;
+            } else if constexpr (CL == 2) {
+                *reinterpret_cast<float2 *>(to + m) = make_float2(bl, bh);
+                *reinterpret_cast<float2 *>(to + NP + m) = make_float2(cl0, ch);
+            } else {
+                *reinterpret_cast<ulonglong2 *>(to) = make_ulonglong2(vB[0], vB[1]);
+                *reinterpret_cast<ulonglong2 *>(to + NP) = make_ulonglong2(vC[0], vC[1]);
+            }
+            lane_reduce<4, NL, PARTS>(v, lane);
+            float *part = reinterpret_cast<float *>(sp + (t * PARTS + ln % PARTS) * PR + pr);
+            if constexpr (NL == 1) *reinterpret_cast<float4 *>(part) = make_float4(v[0], v[1], v[2], v[3]);
+            else if constexpr (NL == 2) *reinterpret_cast<float2 *>(part + reduced_first<4, NL, PARTS>(lane)) = make_float2(v[0], v[1]);
+            else if (reduced_owner<4, NL, PARTS>(lane)) part[reduced_first<4, NL, PARTS>(lane)] = v[0];
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) dA[c][p] = add2(dA[c][p], dAt[c][p]);
         __syncthreads();
         // rows of dx and ddelta, and the CTA's share of dB and dC
-        const size_t out = ((size_t)b * a.T + t0 + St::tok(0)) * D + cb.first + St::chan(0);
+        const size_t out = ((size_t)b * a.T + t0 + St::tok(0)) * D + cb.first + St::chan();
+        float dDt[VEC] = {}, dbt[VEC] = {};
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = St::tok(i), c = St::chan(i);
+            const int t = St::tok(i), c = St::chan();
             if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
-            if ((PER * kGradThreads != kTile * St::ROW || !WIDE) && t >= kTile) continue;
-            float fx[VEC], fd[VEC];
-            if constexpr (VEC == 4) {
-                const float4 o0 = *reinterpret_cast<const float4 *>(so + t * CPB + c), o1 = *reinterpret_cast<const float4 *>(so + t * CPB + c + 2);
-                fx[0] = o0.x; fd[0] = o0.y; fx[1] = o0.z; fd[1] = o0.w;
-                fx[2] = o1.x; fd[2] = o1.y; fx[3] = o1.z; fd[3] = o1.w;
-            } else {
-                const float2 o = so[t * CPB + c];
-                fx[0] = o.x;
-                fd[0] = o.y;
-            }
-            if (!full && t0 + t >= n) {
+            if ((PER * kGradThreads != kChunk * St::ROW || !WIDE) && t >= kChunk) continue;
+            const bool real = full || t0 + t < n;
+            float x[VEC], g[VEC], u[VEC], s1[VEC], s2[VEC], fx[VEC], fd[VEC];
+            St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
+            St::get(raw, buf, 2, i, a, cb, b, t0, n, a.dy, g);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) fx[k] = fd[k] = 0.f;
+            for (int k = 0; k < VEC; ++k) {
+                u[k] = reinterpret_cast<const float *>(su + t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS))[(c + k) & 1];
+                s1[k] = s2[k] = 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                const float4 *part = sp + (t * PARTS + q) * PR + c / 2;
+                if constexpr (VEC == 4) {
+                    const float4 p0 = part[0], p1 = part[1];
+                    s1[0] += p0.x; s1[1] += p0.y; s2[0] += p0.z; s2[1] += p0.w;
+                    s1[2] += p1.x; s1[3] += p1.y; s2[2] += p1.z; s2[3] += p1.w;
+                } else {
+                    s1[0] += reinterpret_cast<const float *>(part)[c & 1];
+                    s2[0] += reinterpret_cast<const float *>(part)[2 + (c & 1)];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                fx[k] = real ? fmaf(u[k], s1[k], skip[k] * g[k]) : 0.f;
+                fd[k] = real ? fmaf(s2[k], kLn2, x[k] * s1[k]) * ss[t * CPB + c + k] : 0.f;
+                dbt[k] += fd[k];
+                dDt[k] = fmaf(g[k], x[k], dDt[k]);                     // padding has arrived as 0
             }
             const size_t to = WIDE ? out + i * at.rows : ((size_t)b * a.T + t0 + t) * D + cb.first + c;
             typename St::Vec v;
@@ -374,35 +367,47 @@ __global__ void __launch_bounds__(kGradThreads, 3) grads_kernel(SsmArgs a, BwdWs
             v.set(fd);
             v.store((T *)a.ddelta + to);
         }
-        for (int e = tid; e < kTile * 2 * NP; e += kGradThreads) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            dbs[k] += dbt[k];
+            dDs[k] += dDt[k];
+        }
+        for (int e = tid; e < kChunk * 2 * NP; e += kGradThreads) {
             const int t = e / (2 * NP), k = e % (2 * NP);
             if (t0 + t >= n || t0 + t >= t_stop) continue;
             float f = 0.f;
 #pragma unroll
-            for (int q = 0; q < kGradWarps; ++q) f += sr[(q * kTile + t) * 2 * NP + k];
+            for (int q = 0; q < kGradWarps; ++q) f += sr[(q * kChunk + t) * 2 * NP + k];
             ws[w.dbc + ((((size_t)b * a.T + t0 + t) * a.G + cb.group) * w.nb + blk % w.nb) * 2 * NP + k] = f;
         }
     }
-    // whole tiles of padding
-    const int done = t_begin + tiles * kTile;
+    // whole chunks of padding
+    const int done = t_begin + chunks * kChunk;
     for (int64_t e = tid; e < (int64_t)max(t_stop - done, 0) * cb.count; e += kGradThreads) {
         const size_t at = ((size_t)b * a.T + done + e / cb.count) * D + cb.first + e % cb.count;
         ((T *)a.dx)[at] = from_f<T>(0.f);
         ((T *)a.ddelta)[at] = from_f<T>(0.f);
     }
     // one row of partials per (sequence, segment): dA [D][N], dD [D], dbias [D]
-    float tot[4] = {myc ? 0.f : dDs, myc ? dDs : 0.f, myc ? 0.f : dbs, myc ? dbs : 0.f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lane_reduce<1, LN, 1>(tot + i, lane);
     float *row = ws + w.par + ((size_t)b * S + seg) * D * (N + 2);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         scatter(row, cb.first + c0 + c, c, dA[c]);
         if (seg == 0 && a.dS0) scatter(a.dS0, bd + c, c, dh[c]);
-        if (ln == 0 && c0 + c < cb.count) {
-            row[(size_t)D * N + cb.first + c0 + c] = tot[c];
-            row[(size_t)D * N + D + cb.first + c0 + c] = tot[2 + c];
-        }
+    }
+    float *sums = reinterpret_cast<float *>(sp);                       // [threads][2 VEC]
+    __syncthreads();                                                   // the last rows have been written
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        sums[tid * 2 * VEC + k] = dDs[k];
+        sums[tid * 2 * VEC + VEC + k] = dbs[k];
+    }
+    __syncthreads();
+    for (int e = tid; e < 2 * CPB; e += kGradThreads) {
+        const int which = e / CPB, c = e % CPB;
+        float f = 0.f;
+        for (int q = 0; q < kGradThreads / St::ROW; ++q) f += sums[(q * St::ROW + c / VEC) * 2 * VEC + which * VEC + c % VEC];
+        if (c < cb.count) row[(size_t)D * N + which * D + cb.first + c] = f;
     }
 }
 
@@ -425,7 +430,8 @@ template <typename T> __global__ void __launch_bounds__(kSumThreads) groups_kern
 
 template <typename T, int LN, bool WIDE> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
-    const size_t smem = Staging<T, kGradThreads, CPB, NP, 3, WIDE>::BYTES + kTile * (pair_row(PAIRS) * 4 + CPB * 4 + PAIRS * 2 + 8 * NP + kGradWarps * 2 * NP) * sizeof(float);
+    const size_t smem = Staging<T, kGradThreads, kChunk, CPB, NP, 3, WIDE>::BYTES +
+                        kChunk * (4 * pair_row(PAIRS) + 4 * sum_parts(LN) * part_row(LN) + 2 * PAIRS + CPB + 8 * NP + kGradWarps * 2 * NP) * sizeof(float);
     const cudaError_t e = allow_smem(grads_kernel<T, LN, WIDE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));

@@ -86,7 +86,7 @@ template <int VEC> __device__ __forceinline__ void step_sizes(float (&u)[VEC], c
     }
 }
 
-// A tile of tokens on its way from global to shared memory: NA token arrays and B and C.  The raw
+// A tile of TILE tokens on its way from global to shared memory: NA token arrays and B and C.  The raw
 // tile arrives by asynchronous copies, two tiles ahead, in one of kStages buffers; every thread
 // then reads back what it copied itself (so its own wait is enough), converts it and stages it
 // for the CTA.  A thread moves PER accesses of VEC channels per array; B and C go four states at a
@@ -94,23 +94,23 @@ template <int VEC> __device__ __forceinline__ void step_sizes(float (&u)[VEC], c
 // WIDE) have no aligned accesses: they are read one by one when they are staged.
 constexpr int kStages = 3;
 
-template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct Staging {
+template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, bool WIDE> struct Staging {
     static constexpr int VEC = WIDE ? 4 : 1;
     static constexpr int ROW = CPB / VEC;                              // accesses a token
-    static constexpr int PER = (kTile * ROW + THREADS - 1) / THREADS;
-    static constexpr int GROW = NP / 4, GALL = 2 * kTile * GROW;       // accesses of B a token; of both in all
+    static constexpr int PER = (TILE * ROW + THREADS - 1) / THREADS;
+    static constexpr int GROW = NP / 4, GALL = 2 * TILE * GROW;       // accesses of B a token; of both in all
     static constexpr int GPER = (GALL + THREADS - 1) / THREADS;
-    static constexpr bool FIXED = THREADS % ROW == 0;                  // a thread's channels are the same every time
-    static constexpr int STAGE = WIDE ? (NA * kTile * CPB + 2 * kTile * NP) : 0;   // elements of a raw tile
+    static_assert(THREADS % ROW == 0);                                 // a thread's channels are the same every time
+    static constexpr int STAGE = WIDE ? (NA * TILE * CPB + 2 * TILE * NP) : 0;   // elements of a raw tile
     static constexpr size_t BYTES = (size_t)kStages * STAGE * sizeof(T);
     using Vec = Pack<T, VEC>;
 
     __device__ __forceinline__ static int tok(int i) { return (threadIdx.x + i * THREADS) / ROW; }
-    __device__ __forceinline__ static int chan(int i) { return (threadIdx.x + i * THREADS) % ROW * VEC; }
+    __device__ __forceinline__ static int chan() { return threadIdx.x % ROW * VEC; }
 
-    // The parameter p (or 0) of the channels of access i.
-    __device__ __forceinline__ static void param(const float *p, const ChannelBlock &cb, int i, float (&f)[VEC]) {
-        const int c = chan(i);
+    // The parameter p (or 0) of the thread's channels.
+    __device__ __forceinline__ static void param(const float *p, const ChannelBlock &cb, float (&f)[VEC]) {
+        const int c = chan();
 #pragma unroll
         for (int k = 0; k < VEC; ++k) f[k] = p && c + k < cb.count ? p[cb.first + c + k] : 0.f;
     }
@@ -118,7 +118,7 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
         return (const T *)(which ? a.Cm : a.Bm) + (((size_t)b * a.T + t) * a.G + cb.group) * a.N;
     }
     // Whether the whole tile at t0 is real: no padding, no channels beyond the block's.
-    __device__ __forceinline__ static bool full(const ChannelBlock &cb, int t0, int n) { return t0 + kTile <= n && cb.count == CPB; }
+    __device__ __forceinline__ static bool full(const ChannelBlock &cb, int t0, int n) { return t0 + TILE <= n && cb.count == CPB; }
     // A thread's place in the arrays, moved from tile to tile: addresses are worked out once.
     struct Cursor {
         const T *p[NA], *g[GPER];
@@ -126,13 +126,12 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
         __device__ __forceinline__ Cursor(const SsmArgs &a, const ChannelBlock &cb, int b, int t0, const void *const (&src)[NA]) {
             rows = (size_t)(THREADS / ROW) * a.D;
             if constexpr (WIDE) {
-                static_assert(FIXED);
-                const ptrdiff_t at = ((ptrdiff_t)b * a.T + t0 + tok(0)) * a.D + cb.first + chan(0);
+                const ptrdiff_t at = ((ptrdiff_t)b * a.T + t0 + tok(0)) * a.D + cb.first + chan();
 #pragma unroll
                 for (int j = 0; j < NA; ++j) p[j] = (const T *)src[j] + at;
 #pragma unroll
                 for (int i = 0; i < GPER; ++i) {
-                    const int e = threadIdx.x + i * THREADS, which = e / (kTile * GROW), r = e % (kTile * GROW);
+                    const int e = threadIdx.x + i * THREADS, which = e / (TILE * GROW), r = e % (TILE * GROW);
                     g[i] = (const T *)(which ? a.Cm : a.Bm) + (((ptrdiff_t)b * a.T + t0 + r / GROW) * a.G + cb.group) * a.N + r % GROW * 4;
                 }
             }
@@ -140,9 +139,9 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
         __device__ __forceinline__ void move(const SsmArgs &a, int tiles) {
             if constexpr (WIDE) {
 #pragma unroll
-                for (int j = 0; j < NA; ++j) p[j] += (ptrdiff_t)tiles * kTile * a.D;
+                for (int j = 0; j < NA; ++j) p[j] += (ptrdiff_t)tiles * TILE * a.D;
 #pragma unroll
-                for (int i = 0; i < GPER; ++i) g[i] += (ptrdiff_t)tiles * kTile * a.G * a.N;
+                for (int i = 0; i < GPER; ++i) g[i] += (ptrdiff_t)tiles * TILE * a.G * a.N;
             }
         }
     };
@@ -158,24 +157,25 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
                     for (int j = 0; j < NA; ++j) {
 #pragma unroll
                         for (int i = 0; i < PER; ++i)
-                            if (PER * THREADS == kTile * ROW || tok(i) < kTile)
-                                copy_async<4 * sizeof(T)>(to + j * kTile * CPB + i * THREADS * 4, at.p[j] + i * at.rows);
+                            if (PER * THREADS == TILE * ROW || tok(i) < TILE)
+                                copy_async<4 * sizeof(T)>(to + j * TILE * CPB + i * THREADS * 4, at.p[j] + i * at.rows);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        if (tok(i) >= kTile) break;
-                        const bool on = t0 + tok(i) < n && chan(0) < cb.count;
+                        if (tok(i) >= TILE) break;
+                        const bool on = t0 + tok(i) < n && chan() < cb.count;
 #pragma unroll
                         for (int j = 0; j < NA; ++j)
-                            copy_async<4 * sizeof(T)>(to + j * kTile * CPB + i * THREADS * 4, on ? at.p[j] + i * at.rows : at.p[j], on);
+                            copy_async<4 * sizeof(T)>(to + j * TILE * CPB + i * THREADS * 4, on ? at.p[j] + i * at.rows : (const T *)a.x, on);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < GPER; ++i) {
-                    const int e = threadIdx.x + i * THREADS, r = e % (kTile * GROW);
+                    const int e = threadIdx.x + i * THREADS, r = e % (TILE * GROW);
+                    const bool on = t0 + r / GROW < n && r % GROW * 4 < a.N;
                     if (e < (both ? GALL : GALL / 2))
-                        copy_async<4 * sizeof(T)>(to + NA * kTile * CPB + i * THREADS * 4, at.g[i], t0 + r / GROW < n && r % GROW * 4 < a.N);
+                        copy_async<4 * sizeof(T)>(to + NA * TILE * CPB + i * THREADS * 4, on ? at.g[i] : (const T *)a.Bm, on);
                 }
                 at.move(a, step);
             }
@@ -185,10 +185,10 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
     // Access i of token array j of the tile at t0, in buffer `buf`.
     __device__ __forceinline__ static void get(const T *raw, int buf, int j, int i, const SsmArgs &a, const ChannelBlock &cb, int b,
                                                int t0, int n, const void *src, float (&f)[VEC]) {
-        const int t = tok(i), c = chan(i);
+        const int t = tok(i), c = chan();
         Vec v;
         if constexpr (WIDE) {
-            v.load(raw + (size_t)buf * STAGE + j * kTile * CPB + (threadIdx.x + i * THREADS) * 4);
+            v.load(raw + (size_t)buf * STAGE + j * TILE * CPB + (threadIdx.x + i * THREADS) * 4);
         } else {
             v.zero();
             if (t0 + t < n && c < cb.count) v.load((const T *)src + ((size_t)b * a.T + t0 + t) * a.D + cb.first + c);
@@ -202,13 +202,13 @@ template <typename T, int THREADS, int CPB, int NP, int NA, bool WIDE> struct St
                                                       int n, bool both, F put) {
 #pragma unroll
         for (int i = 0; i < GPER; ++i) {
-            const int e = threadIdx.x + i * THREADS, which = e / (kTile * GROW), r = e % (kTile * GROW);
+            const int e = threadIdx.x + i * THREADS, which = e / (TILE * GROW), r = e % (TILE * GROW);
             const int t = r / GROW, k = r % GROW * 4;
             if (e >= (both ? GALL : GALL / 2)) break;
             float f[4];
             if constexpr (WIDE) {
                 Pack<T, 4> v;
-                v.load(raw + (size_t)buf * STAGE + NA * kTile * CPB + e * 4);
+                v.load(raw + (size_t)buf * STAGE + NA * TILE * CPB + e * 4);
                 v.get(f);
             } else {
                 const T *p = groups(a, cb, b, t0 + t, which) + k;
@@ -235,24 +235,27 @@ struct ScanWs {
     float *chk, *ucum;  // [chunks]: the state entering a chunk, and u summed from the segment's start
 };
 
-// Row of the staged y: bank of a (token, channel pair) free of conflicts.
-__host__ __device__ constexpr int scan_row(int LN) { return 256 / LN + (LN < 4 ? 0 : LN < 32 ? 64 / LN : 4); }
+// A sum over n is split over LN lanes.  Shuffles join it down to PARTS lanes, which leave their
+// parts in shared memory for whoever writes the result: joining all of it by shuffles costs a
+// tenth of the instructions more.
+__host__ __device__ constexpr int sum_parts(int LN) { return LN < 4 ? LN : 4; }
+// Row of the parts of y, free of bank conflicts.
+__host__ __device__ constexpr int scan_row(int LN) { return 256 / LN + (LN == 2 ? 16 : LN <= 8 ? 8 : 4); }
 
 template <typename T, int LN, bool WIDE, int MODE>
 __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split sp, ScanWs w) {
     constexpr int PAIRS = kScanThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
     constexpr bool OUT = MODE == kOutputs, SEG = MODE == kSegCheckpoints, CHK = SEG || MODE == kCheckpoints;
     constexpr bool BOTH = OUT || SEG;                                  // C is needed
-    constexpr int TB = LN < 16 ? LN / 2 : 8, CNT = 2 * TB;             // tokens and sums over n joined at once
-    constexpr int YS = scan_row(LN);
-    using St = Staging<T, kScanThreads, CPB, NP, SEG ? 3 : 2, WIDE>;
+    constexpr int PARTS = sum_parts(LN), NL = LN / PARTS, YS = scan_row(LN);
+    using St = Staging<T, kScanThreads, kTile, CPB, NP, SEG ? 3 : 2, WIDE>;
     constexpr int VEC = St::VEC, PER = St::PER;
     extern __shared__ float4 smem4[];
     T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
     float4 *su = smem4 + St::BYTES / 16;                               // [kTile][pair_row] (u0, u1, u0 x0, u1 x1)
     float *sB = reinterpret_cast<float *>(su + kTile * pair_row(PAIRS));  // [kTile][NP]
     float *sC = sB + kTile * NP;                                       // [kTile][NP]         BOTH
-    float *sy = sC + kTile * NP;                                       // [kTile][YS] y       OUT
+    float *sy = sC + kTile * NP;                                       // [kTile][PARTS][YS] y OUT
     float *sg = sy;                                                    // [kTile][CPB] dy     SEG
 
     const int lane = threadIdx.x & 31, ln = threadIdx.x % LN, pr = threadIdx.x / LN, seg = blockIdx.y;
@@ -308,17 +311,15 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
     }
 
     float bias[VEC], skip[VEC];
-    if (St::FIXED) {
-        St::param(a.delta_bias, cb, 0, bias);
-        if (OUT) St::param(a.Dskip, cb, 0, skip);
-    }
+    St::param(a.delta_bias, cb, bias);
+    if (OUT) St::param(a.Dskip, cb, skip);
     auto cursor = [&] {
         if constexpr (SEG) return typename St::Cursor(a, cb, b, t_begin, {a.x, a.delta, a.dy});
         else return typename St::Cursor(a, cb, b, t_begin, {a.x, a.delta});
     };
     typename St::Cursor at = cursor();
     auto issue = [&](int t0, int buf) { St::issue(at, raw, buf, a, cb, t0, t0 < t_end, n, BOTH, 1); };
-    T *y = OUT ? (T *)a.y + ((size_t)b * a.T + t_begin + St::tok(0)) * D + cb.first + St::chan(0) : nullptr;
+    T *y = OUT ? (T *)a.y + ((size_t)b * a.T + t_begin + St::tok(0)) * D + cb.first + St::chan() : nullptr;
     f32x2 U = 0;                                                       // of the two channels
     issue(t_begin, 0);
     issue(t_begin + kTile, 1);
@@ -329,10 +330,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         const bool full = St::full(cb, t0, n);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = St::tok(i), c = St::chan(i);
+            const int t = St::tok(i), c = St::chan();
             if (t >= kTile) break;
             float u[VEC], x[VEC];
-            if (!St::FIXED) St::param(a.delta_bias, cb, i, bias);
             St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
             St::get(raw, buf, 1, i, a, cb, b, t0, n, a.delta, u);
             step_sizes<VEC>(u, bias, a.softplus);
@@ -374,40 +374,37 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                     if (c0 + 1 < cb.count) w.ucum[row + 1] = u1;
                 }
             }
-            constexpr int UNROLL = kChunk / TB;
-#pragma unroll UNROLL
-            for (int tb = 0; tb < kChunk; tb += TB) {
-                float v[CNT];
 #pragma unroll
-                for (int k = 0; k < TB; ++k) {
-                    const int t = tc + tb + k;
-                    const float4 q = mine[t * pair_row(PAIRS)];
-                    const ulonglong2 Bq = *reinterpret_cast<const ulonglong2 *>(sB + t * NP + ln * 4);
-                    const ulonglong2 Cq = BOTH ? *reinterpret_cast<const ulonglong2 *>(sC + t * NP + ln * 4) : ulonglong2{};
-                    const f32x2 Bv[2] = {Bq.x, Bq.y}, Cv[2] = {Cq.x, Cq.y};
-                    if (MODE == kEnds || SEG) U = add2(U, pk(q.x, q.y));
-                    const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
+            for (int k = 0; k < kChunk; ++k) {
+                const int t = tc + k;
+                const float4 q = mine[t * pair_row(PAIRS)];
+                const ulonglong2 Bq = *reinterpret_cast<const ulonglong2 *>(sB + t * NP + ln * 4);
+                const ulonglong2 Cq = BOTH ? *reinterpret_cast<const ulonglong2 *>(sC + t * NP + ln * 4) : ulonglong2{};
+                const f32x2 Bv[2] = {Bq.x, Bq.y}, Cv[2] = {Cq.x, Cq.y};
+                float v[2];
+                if (MODE == kEnds || SEG) U = add2(U, pk(q.x, q.y));
+                const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        f32x2 acc = 0;
-                        const float g = SEG ? sg[t * CPB + c0 + c] : 0.f;
+                for (int c = 0; c < 2; ++c) {
+                    f32x2 acc = 0;
+                    const float g = SEG ? sg[t * CPB + c0 + c] : 0.f;
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const f32x2 av = decay2(uu[c], A2[c][p]);
-                            h[c][p] = fma2(av, h[c][p], mul2(ux[c], Bv[p]));
-                            if (OUT) acc = p ? fma2(Cv[p], h[c][p], acc) : mul2(Cv[p], h[c][p]);
-                            if (SEG) {
-                                P[c][p] = mul2(P[c][p], av);
-                                R[c][p] = fma2(P[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
-                            }
+                    for (int p = 0; p < 2; ++p) {
+                        const f32x2 av = decay2(uu[c], A2[c][p]);
+                        h[c][p] = fma2(av, h[c][p], mul2(ux[c], Bv[p]));
+                        if (OUT) acc = p ? fma2(Cv[p], h[c][p], acc) : mul2(Cv[p], h[c][p]);
+                        if (SEG) {
+                            P[c][p] = mul2(P[c][p], av);
+                            R[c][p] = fma2(P[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
                         }
-                        if (OUT) v[2 * k + c] = sum2(acc);
                     }
+                    if (OUT) v[c] = sum2(acc);
                 }
                 if (OUT) {
-                    lane_reduce<CNT, LN, 1>(v, lane);
-                    const int first = reduced_first<CNT, LN, 1>(lane);  // 2 k + c of v[0]
-                    if (reduced_owner<CNT, LN, 1>(lane)) sy[(tc + tb + first / 2) * YS + c0 + (first & 1)] = v[0];
+                    lane_reduce<2, NL, PARTS>(v, lane);
+                    float *to = sy + (t * PARTS + ln % PARTS) * YS + c0;
+                    if constexpr (NL == 1) *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
+                    else if (reduced_owner<2, NL, PARTS>(lane)) to[reduced_first<2, NL, PARTS>(lane)] = v[0];
                 }
             }
         }
@@ -415,17 +412,19 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         if constexpr (OUT) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int t = St::tok(i), c = St::chan(i);
+                const int t = St::tok(i), c = St::chan();
                 if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
                 if ((PER * kScanThreads != kTile * St::ROW || !WIDE) && t >= kTile) continue;
-                if (!St::FIXED) St::param(a.Dskip, cb, i, skip);
                 float f[VEC], x[VEC];
                 St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
-                if constexpr (VEC == 4) {
-                    const float4 q = *reinterpret_cast<const float4 *>(sy + t * YS + c);
-                    f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
-                } else {
-                    f[0] = sy[t * YS + c];
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) {
+                    Pack<float, VEC> part;
+                    float g[VEC];
+                    part.load(sy + (t * PARTS + q) * YS + c);
+                    part.get(g);
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) f[k] = q ? f[k] + g[k] : g[k];
                 }
                 if (a.Dskip) {
 #pragma unroll
@@ -482,8 +481,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
 template <typename T, int LN, bool WIDE, int MODE>
 cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
     constexpr int CPB = 2 * kScanThreads / LN, NP = 4 * LN, YS = scan_row(LN);
-    using St = Staging<T, kScanThreads, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, WIDE>;
-    const size_t smem = St::BYTES + kTile * (4 * pair_row(CPB / 2) + 2 * NP + YS) * sizeof(float);
+    using St = Staging<T, kScanThreads, kTile, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, WIDE>;
+    const size_t smem = St::BYTES + kTile * (4 * pair_row(CPB / 2) + 2 * NP + sum_parts(LN) * YS) * sizeof(float);
     const cudaError_t e = allow_smem(scan_kernel<T, LN, WIDE, MODE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
