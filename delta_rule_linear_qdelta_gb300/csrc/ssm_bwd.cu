@@ -169,18 +169,28 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
     auto issue = [&](int c, int buf) { St::issue(at, raw, buf, a, cb, t_begin + c * kChunk, c >= 0, n, true, -1); };
     issue(chunks - 1, 0);
     issue(chunks - 2, 1);
+    // this thread's first row of dx and ddelta, and the CTA's of the partial dB and dC, of the chunk at hand
+    const int last = t_begin + (chunks - 1) * kChunk;
+    size_t out = ((size_t)b * a.T + last + St::tok(0)) * D + cb.first + St::chan();
+    const size_t dbc_row = (size_t)a.G * w.nb * 2 * NP;
+    float *dbc = ws + w.dbc + ((size_t)b * a.T + last) * dbc_row + ((size_t)cb.group * w.nb + blk % w.nb) * 2 * NP;
     // the checkpoint of the next chunk is on its way while one is computed
     float4 ck_h[2];
     float ck_u[2];
-    auto checkpoint = [&](int t) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const size_t row = (size_t)(t / kChunk) * all + (size_t)b * D + cb.first + min(c0 + c, cb.count - 1);
-            ck_h[c] = *reinterpret_cast<const float4 *>(ws + w.chk + row * NP + ln * 4);
-            if (S > 1) ck_u[c] = ws[w.ucum + row];
+    const int c1 = min(c0 + 1, cb.count - 1), cz = min(c0, cb.count - 1);
+    const float *ck_at = ws + w.chk + ((size_t)(last / kChunk) * all + (size_t)b * D + cb.first + cz) * NP + ln * 4;
+    const float *cu_at = ws + w.ucum + (size_t)(last / kChunk) * all + (size_t)b * D + cb.first + cz;
+    auto checkpoint = [&] {
+        ck_h[0] = *reinterpret_cast<const float4 *>(ck_at);
+        ck_h[1] = *reinterpret_cast<const float4 *>(ck_at + (c1 - cz) * NP);
+        if (seg > 0) {
+            ck_u[0] = cu_at[0];
+            ck_u[1] = cu_at[c1 - cz];
         }
+        ck_at -= all * NP;
+        cu_at -= all;
     };
-    if (chunks) checkpoint(t_begin + (chunks - 1) * kChunk);
+    if (chunks) checkpoint();
     int buf = 0;
     for (int chunk = chunks - 1; chunk >= 0; --chunk, buf = buf + 1 < kStages ? buf + 1 : 0) {
         const int t0 = t_begin + chunk * kChunk;
@@ -243,7 +253,7 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
                 for (int p = 0; p < 2; ++p) h0[c][p] = fma2(decay2(pk(U, U), A2[c][p]), hin[c][p], h0[c][p]);
             }
         }
-        if (chunk > 0) checkpoint(t0 - kChunk);
+        if (chunk > 0) checkpoint();
 #pragma unroll
         for (int k = 0; k < kChunk; ++k) {
             const float4 q = mine[k * pair_row(PAIRS)];
@@ -325,61 +335,78 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
             for (int p = 0; p < 2; ++p) dA[c][p] = add2(dA[c][p], dAt[c][p]);
         __syncthreads();
         // rows of dx and ddelta, and the CTA's share of dB and dC
-        const size_t out = ((size_t)b * a.T + t0 + St::tok(0)) * D + cb.first + St::chan();
-        float dDt[VEC] = {}, dbt[VEC] = {};
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int t = St::tok(i), c = St::chan();
             if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
             if ((PER * kGradThreads != kChunk * St::ROW || !WIDE) && t >= kChunk) continue;
-            const bool real = full || t0 + t < n;
-            float x[VEC], g[VEC], u[VEC], s1[VEC], s2[VEC], fx[VEC], fd[VEC];
+            float x[VEC], g[VEC], u[VEC], sig[VEC], s1[VEC], s2[VEC];
             St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
             St::get(raw, buf, 2, i, a, cb, b, t0, n, a.dy, g);
+            Pack<float, VEC> sv;
+            sv.load(ss + t * CPB + c);
+            sv.get(sig);
+            const float4 *up = su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS), *part = sp + t * PARTS * PR + c / 2;
+            if constexpr (VEC == 4) {
+                const float4 u0 = up[0], u1 = up[PAIRS / 2 + 4];       // an even pair and the odd one after it
+                u[0] = u0.x; u[1] = u0.y; u[2] = u1.x; u[3] = u1.y;
+                ulonglong2 p0 = {}, p1 = {};
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                u[k] = reinterpret_cast<const float *>(su + t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS))[(c + k) & 1];
-                s1[k] = s2[k] = 0.f;
-            }
+                for (int q = 0; q < PARTS; ++q) {
+                    const ulonglong2 q0 = *reinterpret_cast<const ulonglong2 *>(part + q * PR);
+                    const ulonglong2 q1 = *reinterpret_cast<const ulonglong2 *>(part + q * PR + 1);
+                    p0 = q ? make_ulonglong2(add2(p0.x, q0.x), add2(p0.y, q0.y)) : q0;
+                    p1 = q ? make_ulonglong2(add2(p1.x, q1.x), add2(p1.y, q1.y)) : q1;
+                }
+                unpk(p0.x, s1[0], s1[1]);
+                unpk(p0.y, s2[0], s2[1]);
+                unpk(p1.x, s1[2], s1[3]);
+                unpk(p1.y, s2[2], s2[3]);
+            } else {
+                u[0] = reinterpret_cast<const float *>(up)[c & 1];
+                s1[0] = s2[0] = 0.f;
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) {
-                const float4 *part = sp + (t * PARTS + q) * PR + c / 2;
-                if constexpr (VEC == 4) {
-                    const float4 p0 = part[0], p1 = part[1];
-                    s1[0] += p0.x; s1[1] += p0.y; s2[0] += p0.z; s2[1] += p0.w;
-                    s1[2] += p1.x; s1[3] += p1.y; s2[2] += p1.z; s2[3] += p1.w;
-                } else {
-                    s1[0] += reinterpret_cast<const float *>(part)[c & 1];
-                    s2[0] += reinterpret_cast<const float *>(part)[2 + (c & 1)];
+                for (int q = 0; q < PARTS; ++q) {
+                    s1[0] += reinterpret_cast<const float *>(part + q * PR)[c & 1];
+                    s2[0] += reinterpret_cast<const float *>(part + q * PR)[2 + (c & 1)];
                 }
             }
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
-                fx[k] = real ? fmaf(u[k], s1[k], skip[k] * g[k]) : 0.f;
-                fd[k] = real ? fmaf(s2[k], kLn2, x[k] * s1[k]) * ss[t * CPB + c + k] : 0.f;
-                dbt[k] += fd[k];
-                dDt[k] = fmaf(g[k], x[k], dDt[k]);                     // padding has arrived as 0
+                const float f = s1[k];
+                s1[k] = fmaf(u[k], f, skip[k] * g[k]);                 // dx
+                s2[k] = fmaf(s2[k], kLn2, x[k] * f) * sig[k];          // ddelta
+            }
+            if (!full && t0 + t >= n) {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) s1[k] = s2[k] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                dbs[k] += s2[k];
+                dDs[k] = fmaf(g[k], x[k], dDs[k]);                     // padding has arrived as 0
             }
             const size_t to = WIDE ? out + i * at.rows : ((size_t)b * a.T + t0 + t) * D + cb.first + c;
             typename St::Vec v;
-            v.set(fx);
+            v.set(s1);
             v.store((T *)a.dx + to);
-            v.set(fd);
+            v.set(s2);
             v.store((T *)a.ddelta + to);
         }
+        out -= (size_t)kChunk * D;
+        for (int e = tid; e < kChunk * 2 * NP / 4; e += kGradThreads) {
+            const int t = e / (NP / 2), k = e % (NP / 2) * 4;
+            if (!full && (t0 + t >= n || t0 + t >= t_stop)) continue;
+            const float *p = sr + t * 2 * NP + k;
+            ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(p);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            dbs[k] += dbt[k];
-            dDs[k] += dDt[k];
+            for (int q = 1; q < kGradWarps; ++q) {
+                const ulonglong2 g = *reinterpret_cast<const ulonglong2 *>(p + q * kChunk * 2 * NP);
+                f = make_ulonglong2(add2(f.x, g.x), add2(f.y, g.y));
+            }
+            *reinterpret_cast<ulonglong2 *>(dbc + t * dbc_row + k) = f;
         }
-        for (int e = tid; e < kChunk * 2 * NP; e += kGradThreads) {
-            const int t = e / (2 * NP), k = e % (2 * NP);
-            if (t0 + t >= n || t0 + t >= t_stop) continue;
-            float f = 0.f;
-#pragma unroll
-            for (int q = 0; q < kGradWarps; ++q) f += sr[(q * kChunk + t) * 2 * NP + k];
-            ws[w.dbc + ((((size_t)b * a.T + t0 + t) * a.G + cb.group) * w.nb + blk % w.nb) * 2 * NP + k] = f;
-        }
+        dbc -= kChunk * dbc_row;
     }
     // whole chunks of padding
     const int done = t_begin + chunks * kChunk;
