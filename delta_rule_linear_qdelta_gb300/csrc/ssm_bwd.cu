@@ -70,8 +70,11 @@ BwdWs bwd_ws(int B, int T, int D, int G, int N) {
 // of its channel bits, so what it gives away is always its upper half and nothing has to be
 // selected; B and C lie in shared memory in all four orders.  The sums over n behind dx and
 // ddelta are left as parts in shared memory for the thread that writes the rows.
-// Row of the parts: float4 (s1 of both channels, s2 of both), free of bank conflicts.
-__host__ __device__ constexpr int part_row(int LN) { return kGradThreads / LN + (LN == 2 ? 4 : 2); }
+// Row of the parts: float4 (s1 of both channels, s2 of both) of pair p at pair_at(p).  This length
+// and order_size bring the lanes that shared memory serves at once to different banks.
+__host__ __device__ constexpr int part_row(int LN) { return pair_row(kGradThreads / LN) + (LN == 2 ? 2 : 1); }
+// From B (or C) in one order to the next.
+__host__ __device__ constexpr int order_size(int NP) { return kChunk * NP + 8; }
 
 template <typename T, int LN, bool WIDE>
 __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
@@ -86,8 +89,8 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
     float2 *sg = reinterpret_cast<float2 *>(sp + kChunk * PARTS * PR); // [kChunk][PAIRS] (g0, g1)
     float *ss = reinterpret_cast<float *>(sg + kChunk * PAIRS);        // [kChunk][CPB] softplus'
     float *sB = ss + kChunk * CPB;                                     // [4 orders][kChunk][NP]
-    float *sC = sB + 4 * kChunk * NP;
-    float *sr = sC + 4 * kChunk * NP;                                  // [warps][kChunk][2 NP] (dB, dC)
+    float *sC = sB + 4 * order_size(NP);
+    float *sr = sC + 4 * order_size(NP);                                  // [warps][kChunk][2 NP] (dB, dC)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ln = tid % LN, pr = tid / LN, seg = blockIdx.y;
     const int cl = lane / LN, m = (CL >= 2 ? (cl & 1) * 2 : 0) + (CL >= 4 ? cl >> 1 & 1 : 0);
@@ -236,10 +239,10 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
         St::get_groups(raw, buf, a, cb, b, t0, n, true, [&](int which, int t, int k, const float (&f)[4]) {
 #pragma unroll
             for (int o = 0; o < 4; ++o)
-                *reinterpret_cast<float4 *>((which ? sC : sB) + (o * kChunk + t) * NP + k) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
+                *reinterpret_cast<float4 *>((which ? sC : sB) + o * order_size(NP) + t * NP + k) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
         });
         const float4 *mine = su + pair_at(pr, PAIRS);
-        const float *gB = sB + m * kChunk * NP + ln * 4, *gC = sC + m * kChunk * NP + ln * 4;
+        const float *gB = sB + m * order_size(NP) + ln * 4, *gC = sC + m * order_size(NP) + ln * 4;
         __syncthreads();
 
         f32x2 h0[2][2], hh[kChunk][2][2], dAt[2][2] = {};              // dAt: the chunk's share; short sums lose less
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
                 *reinterpret_cast<ulonglong2 *>(to + NP) = make_ulonglong2(vC[0], vC[1]);
             }
             lane_reduce<4, NL, PARTS>(v, lane);
-            float *part = reinterpret_cast<float *>(sp + (t * PARTS + ln % PARTS) * PR + pr);
+            float *part = reinterpret_cast<float *>(sp + (t * PARTS + ln % PARTS) * PR + pair_at(pr, PAIRS));
             if constexpr (NL == 1) *reinterpret_cast<float4 *>(part) = make_float4(v[0], v[1], v[2], v[3]);
             else if constexpr (NL == 2) *reinterpret_cast<float2 *>(part + reduced_first<4, NL, PARTS>(lane)) = make_float2(v[0], v[1]);
             else if (reduced_owner<4, NL, PARTS>(lane)) part[reduced_first<4, NL, PARTS>(lane)] = v[0];
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
             Pack<float, VEC> sv;
             sv.load(ss + t * CPB + c);
             sv.get(sig);
-            const float4 *up = su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS), *part = sp + t * PARTS * PR + c / 2;
+            const float4 *up = su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS), *part = sp + t * PARTS * PR + pair_at(c / 2, PAIRS);
             if constexpr (VEC == 4) {
                 const float4 u0 = up[0], u1 = up[PAIRS / 2 + 4];       // an even pair and the odd one after it
                 u[0] = u0.x; u[1] = u0.y; u[2] = u1.x; u[3] = u1.y;
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
 #pragma unroll
                 for (int q = 0; q < PARTS; ++q) {
                     const ulonglong2 q0 = *reinterpret_cast<const ulonglong2 *>(part + q * PR);
-                    const ulonglong2 q1 = *reinterpret_cast<const ulonglong2 *>(part + q * PR + 1);
+                    const ulonglong2 q1 = *reinterpret_cast<const ulonglong2 *>(part + q * PR + PAIRS / 2 + 4);
                     p0 = q ? make_ulonglong2(add2(p0.x, q0.x), add2(p0.y, q0.y)) : q0;
                     p1 = q ? make_ulonglong2(add2(p1.x, q1.x), add2(p1.y, q1.y)) : q1;
                 }
@@ -458,7 +461,8 @@ template <typename T> __global__ void __launch_bounds__(kSumThreads) groups_kern
 template <typename T, int LN, bool WIDE> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
     const size_t smem = Staging<T, kGradThreads, kChunk, CPB, NP, 3, WIDE>::BYTES +
-                        kChunk * (4 * pair_row(PAIRS) + 4 * sum_parts(LN) * part_row(LN) + 2 * PAIRS + CPB + 8 * NP + kGradWarps * 2 * NP) * sizeof(float);
+                        kChunk * (4 * pair_row(PAIRS) + 4 * sum_parts(LN) * part_row(LN) + 2 * PAIRS + CPB + kGradWarps * 2 * NP) * sizeof(float) +
+                        8 * order_size(NP) * sizeof(float);
     const cudaError_t e = allow_smem(grads_kernel<T, LN, WIDE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
