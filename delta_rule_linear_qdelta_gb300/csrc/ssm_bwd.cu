@@ -76,12 +76,12 @@ __host__ __device__ constexpr int part_row(int LN) { return pair_row(kGradThread
 // From B (or C) in one order to the next.
 __host__ __device__ constexpr int order_size(int NP) { return kChunk * NP + 8; }
 
-template <typename T, int LN, bool WIDE>
+template <typename T, int LN, int VEC>
 __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN, CL = 32 / LN;
     constexpr int PARTS = sum_parts(LN), NL = LN / PARTS, PR = part_row(LN);
-    using St = Staging<T, kGradThreads, kChunk, CPB, NP, 3, WIDE>;
-    constexpr int VEC = St::VEC, PER = St::PER;
+    using St = Staging<T, kGradThreads, kChunk, CPB, NP, 3, VEC>;
+    constexpr int PER = St::PER;
     extern __shared__ float4 smem4[];
     T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] chunks on their way
     float4 *su = smem4 + St::BYTES / 16;                               // [kChunk][pair_row] (u0, u1, u0 x0, u1 x1)
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
     for (int chunk = chunks - 1; chunk >= 0; --chunk, buf = buf + 1 < kStages ? buf + 1 : 0) {
         const int t0 = t_begin + chunk * kChunk;
         issue(chunk - 2, buf + 2 < kStages ? buf + 2 : buf + 2 - kStages);
-        if constexpr (WIDE) copies_done<2>();
+        if constexpr (St::ASYNC) copies_done<2>();
         const bool full = St::full(cb, t0, n);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -222,12 +222,15 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) u[k] = 0.f;
             }
-            if constexpr (VEC == 4) {
+            if constexpr (VEC > 1) {
 #pragma unroll
-                for (int k = 0; k < 4; k += 2)
+                for (int k = 0; k < VEC; k += 2)
                     su[t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS)] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
-                *reinterpret_cast<float4 *>(ss + t * CPB + c) = make_float4(sig[0], sig[1], sig[2], sig[3]);
-                *reinterpret_cast<float4 *>(sg + t * PAIRS + c / 2) = make_float4(g[0], g[1], g[2], g[3]);
+                Pack<float, VEC> v;
+                v.set(sig);
+                v.store(ss + t * CPB + c);
+                v.set(g);
+                v.store(reinterpret_cast<float *>(sg + t * PAIRS + c / 2));
             } else {
                 float *to = reinterpret_cast<float *>(su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS)) + (c & 1);
                 to[0] = u[0];
@@ -236,10 +239,17 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
                 ss[t * CPB + c] = sig[0];
             }
         }
-        St::get_groups(raw, buf, a, cb, b, t0, n, true, [&](int which, int t, int k, const float (&f)[4]) {
+        St::get_groups(raw, buf, a, cb, b, t0, n, true, [&](int which, int t, int k, const float (&f)[VEC]) {
+            float *to = (which ? sC : sB) + t * NP + k;
 #pragma unroll
-            for (int o = 0; o < 4; ++o)
-                *reinterpret_cast<float4 *>((which ? sC : sB) + o * order_size(NP) + t * NP + k) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
+            for (int o = 0; o < 4; ++o) {
+                if constexpr (VEC == 4) {
+                    *reinterpret_cast<float4 *>(to + o * order_size(NP)) = make_float4(f[o], f[1 ^ o], f[2 ^ o], f[3 ^ o]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) to[o * order_size(NP) - k % 4 + ((k % 4 + j) ^ o)] = f[j];
+                }
+            }
         });
         const float4 *mine = su + pair_at(pr, PAIRS);
         const float *gB = sB + m * order_size(NP) + ln * 4, *gC = sC + m * order_size(NP) + ln * 4;
@@ -342,7 +352,7 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
         for (int i = 0; i < PER; ++i) {
             const int t = St::tok(i), c = St::chan();
             if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
-            if ((PER * kGradThreads != kChunk * St::ROW || !WIDE) && t >= kChunk) continue;
+            if (!St::EVEN && t >= kChunk) continue;
             float x[VEC], g[VEC], u[VEC], sig[VEC], s1[VEC], s2[VEC];
             St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
             St::get(raw, buf, 2, i, a, cb, b, t0, n, a.dy, g);
@@ -366,12 +376,15 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
                 unpk(p1.x, s1[2], s1[3]);
                 unpk(p1.y, s2[2], s2[3]);
             } else {
-                u[0] = reinterpret_cast<const float *>(up)[c & 1];
-                s1[0] = s2[0] = 0.f;
 #pragma unroll
-                for (int q = 0; q < PARTS; ++q) {
-                    s1[0] += reinterpret_cast<const float *>(part + q * PR)[c & 1];
-                    s2[0] += reinterpret_cast<const float *>(part + q * PR)[2 + (c & 1)];
+                for (int k = 0; k < VEC; ++k) {
+                    u[k] = reinterpret_cast<const float *>(up)[(c + k) & 1];
+                    s1[k] = s2[k] = 0.f;
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q) {
+                        s1[k] += reinterpret_cast<const float *>(part + q * PR)[(c + k) & 1];
+                        s2[k] += reinterpret_cast<const float *>(part + q * PR)[2 + ((c + k) & 1)];
+                    }
                 }
             }
 #pragma unroll
@@ -389,7 +402,7 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
                 dbs[k] += s2[k];
                 dDs[k] = fmaf(g[k], x[k], dDs[k]);                     // padding has arrived as 0
             }
-            const size_t to = WIDE ? out + i * at.rows : ((size_t)b * a.T + t0 + t) * D + cb.first + c;
+            const size_t to = out + i * at.rows;
             typename St::Vec v;
             v.set(s1);
             v.store((T *)a.dx + to);
@@ -441,37 +454,59 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
     }
 }
 
-// Launch 3: dB, dC of one (token, group, which, n): the sum over the group's channel blocks.
+// Launch 3: four neighbouring values of dB or dC of one (token, group): the sum over the group's
+// channel blocks.
 template <typename T> __global__ void __launch_bounds__(kSumThreads) groups_kernel(SsmArgs a, BwdWs w, const float *ws, int NP) {
+    const int quads = NP / 2;                                          // of a row: dB [NP], dC [NP]
     const int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x, rows = (int64_t)a.B * a.T * a.G;
-    const int64_t row = i / (2 * NP);
-    const int k = (int)(i % (2 * NP)), which = k / NP, nn = k % NP;
+    const int64_t row = i >> (31 - __clz(quads));                      // quads is a power of two
+    const int k = (int)(i & (quads - 1)) * 4, which = k >= NP, nn = k - which * NP;
     if (row >= rows || nn >= a.N) return;
-    const int64_t bt = row / a.G;
-    const int b = (int)(bt / a.T), t = (int)(bt % a.T);
-    float f = 0.f;
-    if (t < seq_len(a.lens, b, a.T)) {
-        const float *p = ws + w.dbc + (size_t)row * w.nb * 2 * NP + k;
-#pragma unroll 4
-        for (int q = 0; q < w.nb; ++q) f += p[(size_t)q * 2 * NP];
+    bool real = true;
+    if (a.lens) {
+        const int64_t bt = row / a.G;
+        const int b = (int)(bt / a.T);
+        real = bt - (int64_t)b * a.T < seq_len(a.lens, b, a.T);
     }
-    ((T *)(which ? a.dC : a.dB))[row * a.N + nn] = from_f<T>(f);
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (real) {
+        const float *p = ws + w.dbc + (size_t)row * w.nb * 2 * NP + k;
+#pragma unroll 8
+        for (int q = 0; q < w.nb; ++q) {
+            const float4 g = *reinterpret_cast<const float4 *>(p + (size_t)q * 2 * NP);
+            f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
+        }
+    }
+    T *to = (T *)(which ? a.dC : a.dB) + row * a.N + nn;
+    const float e[4] = {f.x, f.y, f.z, f.w};
+    if (a.N % 4 == 0) {
+        Pack<T, 4> v;
+        v.set(e);
+        v.store(to);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (nn + j < a.N) to[j] = from_f<T>(e[j]);
+    }
 }
 
-template <typename T, int LN, bool WIDE> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
+template <typename T, int LN, int VEC> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
-    const size_t smem = Staging<T, kGradThreads, kChunk, CPB, NP, 3, WIDE>::BYTES +
+    const size_t smem = Staging<T, kGradThreads, kChunk, CPB, NP, 3, VEC>::BYTES +
                         kChunk * (4 * pair_row(PAIRS) + 4 * sum_parts(LN) * part_row(LN) + 2 * PAIRS + CPB + kGradWarps * 2 * NP) * sizeof(float) +
                         8 * order_size(NP) * sizeof(float);
-    const cudaError_t e = allow_smem(grads_kernel<T, LN, WIDE>, smem);
+    const cudaError_t e = allow_smem(grads_kernel<T, LN, VEC>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
-    grads_kernel<T, LN, WIDE><<<dim3(nblk, w.sp.S), kGradThreads, smem, s>>>(a, w, (float *)a.ws);
+    grads_kernel<T, LN, VEC><<<dim3(nblk, w.sp.S), kGradThreads, smem, s>>>(a, w, (float *)a.ws);
     return cudaGetLastError();
 }
 template <typename T, int LN> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
-    const bool wide = a.D / a.G % 4 == 0 && a.N % 4 == 0;
-    return wide ? run_grads<T, LN, true>(a, w, s) : run_grads<T, LN, false>(a, w, s);
+    const int v = access_size<T>(a);
+    if (v == 4) return run_grads<T, LN, 4>(a, w, s);
+    if constexpr (sizeof(T) == 2)
+        if (v == 2) return run_grads<T, LN, 2>(a, w, s);
+    return run_grads<T, LN, 1>(a, w, s);
 }
 
 template <typename T> cudaError_t run_bwd(const SsmArgs &a, cudaStream_t s, int *nlaunch) {
@@ -496,7 +531,7 @@ template <typename T> cudaError_t run_bwd(const SsmArgs &a, cudaStream_t s, int 
     }
     if (a.T > 0 && a.B > 0) {
         const int NP = padded_states(a.N);
-        const int64_t items = (int64_t)a.B * a.T * a.G * 2 * NP;
+        const int64_t items = (int64_t)a.B * a.T * a.G * (NP / 2);
         groups_kernel<T><<<(unsigned)((items + kSumThreads - 1) / kSumThreads), kSumThreads, 0, s>>>(a, w, ws, NP);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;

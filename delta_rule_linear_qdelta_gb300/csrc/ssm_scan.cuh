@@ -89,76 +89,88 @@ template <int VEC> __device__ __forceinline__ void step_sizes(float (&u)[VEC], c
 // A tile of TILE tokens on its way from global to shared memory: NA token arrays and B and C.  The raw
 // tile arrives by asynchronous copies, two tiles ahead, in one of kStages buffers; every thread
 // then reads back what it copied itself (so its own wait is enough), converts it and stages it
-// for the CTA.  A thread moves PER accesses of VEC channels per array; B and C go four states at a
-// time.  What is beyond the sequence, the block's channels or N arrives as zero.  Odd shapes (not
-// WIDE) have no aligned accesses: they are read one by one when they are staged.
+// for the CTA.  An access is V neighbouring channels of a token, or V states of its B or C: 4, or for
+// odd shapes 2 (bf16) or 1; single bf16 values are below what a copy can move and are read when they
+// are staged.  What is beyond the sequence, the block's channels or N arrives as zero.
 constexpr int kStages = 3;
 
-template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, bool WIDE> struct Staging {
-    static constexpr int VEC = WIDE ? 4 : 1;
-    static constexpr int ROW = CPB / VEC;                              // accesses a token
+template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, int V> struct Staging {
+    static constexpr bool ASYNC = V * sizeof(T) >= 4;
+    static constexpr int ROW = CPB / V;                                // accesses a token
     static constexpr int PER = (TILE * ROW + THREADS - 1) / THREADS;
-    static constexpr int GROW = NP / 4, GALL = 2 * TILE * GROW;       // accesses of B a token; of both in all
+    static constexpr bool EVEN = PER * THREADS == TILE * ROW;          // every thread has PER of them
+    static constexpr int GROW = NP / V, GALL = 2 * TILE * GROW;        // accesses of B a token; of both in all
     static constexpr int GPER = (GALL + THREADS - 1) / THREADS;
     static_assert(THREADS % ROW == 0);                                 // a thread's channels are the same every time
-    static constexpr int STAGE = WIDE ? (NA * TILE * CPB + 2 * TILE * NP) : 0;   // elements of a raw tile
+    static constexpr int STAGE = ASYNC ? (NA * TILE * CPB + 2 * TILE * NP) : 0;    // elements of a raw tile
     static constexpr size_t BYTES = (size_t)kStages * STAGE * sizeof(T);
-    using Vec = Pack<T, VEC>;
+    using Vec = Pack<T, V>;
 
     __device__ __forceinline__ static int tok(int i) { return (threadIdx.x + i * THREADS) / ROW; }
-    __device__ __forceinline__ static int chan() { return threadIdx.x % ROW * VEC; }
+    __device__ __forceinline__ static int chan() { return threadIdx.x % ROW * V; }
+    // B or C, token and first state of group access i
+    struct Group {
+        int e, which, t, k;
+        __device__ __forceinline__ Group(int i) {
+            e = threadIdx.x + i * THREADS;
+            which = e / (TILE * GROW);
+            t = e % (TILE * GROW) / GROW;
+            k = e % GROW * V;
+        }
+    };
 
     // The parameter p (or 0) of the thread's channels.
-    __device__ __forceinline__ static void param(const float *p, const ChannelBlock &cb, float (&f)[VEC]) {
+    __device__ __forceinline__ static void param(const float *p, const ChannelBlock &cb, float (&f)[V]) {
         const int c = chan();
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) f[k] = p && c + k < cb.count ? p[cb.first + c + k] : 0.f;
-    }
-    __device__ __forceinline__ static const T *groups(const SsmArgs &a, const ChannelBlock &cb, int b, int64_t t, int which) {
-        return (const T *)(which ? a.Cm : a.Bm) + (((size_t)b * a.T + t) * a.G + cb.group) * a.N;
+        for (int k = 0; k < V; ++k) f[k] = p && c + k < cb.count ? p[cb.first + c + k] : 0.f;
     }
     // Whether the whole tile at t0 is real: no padding, no channels beyond the block's.
     __device__ __forceinline__ static bool full(const ChannelBlock &cb, int t0, int n) { return t0 + TILE <= n && cb.count == CPB; }
+
     // A thread's place in the arrays, moved from tile to tile: addresses are worked out once.
     struct Cursor {
-        const T *p[NA], *g[GPER];
-        size_t rows;                                                   // from one access of a tile to the next
+        const T *p[NA], *g[2], *own;                                   // tokens; the tile's B and C; this thread's if it has one access
+        size_t rows;                                                   // from one token access of a tile to the next
+        int group_row;
         __device__ __forceinline__ Cursor(const SsmArgs &a, const ChannelBlock &cb, int b, int t0, const void *const (&src)[NA]) {
             rows = (size_t)(THREADS / ROW) * a.D;
-            if constexpr (WIDE) {
-                const ptrdiff_t at = ((ptrdiff_t)b * a.T + t0 + tok(0)) * a.D + cb.first + chan();
+            group_row = a.G * a.N;
+            const ptrdiff_t at = ((ptrdiff_t)b * a.T + t0 + tok(0)) * a.D + cb.first + chan();
 #pragma unroll
-                for (int j = 0; j < NA; ++j) p[j] = (const T *)src[j] + at;
-#pragma unroll
-                for (int i = 0; i < GPER; ++i) {
-                    const int e = threadIdx.x + i * THREADS, which = e / (TILE * GROW), r = e % (TILE * GROW);
-                    g[i] = (const T *)(which ? a.Cm : a.Bm) + (((ptrdiff_t)b * a.T + t0 + r / GROW) * a.G + cb.group) * a.N + r % GROW * 4;
-                }
-            }
+            for (int j = 0; j < NA; ++j) p[j] = (const T *)src[j] + at;
+            const ptrdiff_t ga = (((ptrdiff_t)b * a.T + t0) * a.G + cb.group) * a.N;
+            g[0] = (const T *)a.Bm + ga;
+            g[1] = (const T *)a.Cm + ga;
+            const Group q(0);
+            own = g[q.which ? 1 : 0] + (ptrdiff_t)q.t * group_row + q.k;
         }
         __device__ __forceinline__ void move(const SsmArgs &a, int tiles) {
-            if constexpr (WIDE) {
 #pragma unroll
-                for (int j = 0; j < NA; ++j) p[j] += (ptrdiff_t)tiles * TILE * a.D;
-#pragma unroll
-                for (int i = 0; i < GPER; ++i) g[i] += (ptrdiff_t)tiles * TILE * a.G * a.N;
-            }
+            for (int j = 0; j < NA; ++j) p[j] += (ptrdiff_t)tiles * TILE * a.D;
+            const ptrdiff_t by = (ptrdiff_t)tiles * TILE * group_row;
+            g[0] += by;
+            g[1] += by;
+            own += by;
+        }
+        // where group access q of the cursor's tile lies
+        __device__ __forceinline__ const T *group(const Group &q) const {
+            return GPER == 1 ? own : g[q.which] + (ptrdiff_t)q.t * group_row + q.k;
         }
     };
     // Starts the copies of the cursor's tile, which is at t0, into buffer `buf` (one group of copies,
     // empty where `any` is false) and moves the cursor by `step` tiles.
     __device__ __forceinline__ static void issue(Cursor &at, T *raw, int buf, const SsmArgs &a, const ChannelBlock &cb, int t0, bool any,
                                                  int n, bool both, int step) {
-        if constexpr (WIDE) {
-            T *to = raw + (size_t)buf * STAGE + threadIdx.x * 4;
+        if constexpr (ASYNC) {
+            T *to = raw + (size_t)buf * STAGE + threadIdx.x * V;
             if (any) {
                 if (full(cb, t0, n)) {
 #pragma unroll
                     for (int j = 0; j < NA; ++j) {
 #pragma unroll
                         for (int i = 0; i < PER; ++i)
-                            if (PER * THREADS == TILE * ROW || tok(i) < TILE)
-                                copy_async<4 * sizeof(T)>(to + j * TILE * CPB + i * THREADS * 4, at.p[j] + i * at.rows);
+                            if (EVEN || tok(i) < TILE) copy_async<V * sizeof(T)>(to + j * TILE * CPB + i * THREADS * V, at.p[j] + i * at.rows);
                     }
                 } else {
 #pragma unroll
@@ -167,55 +179,54 @@ template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, bool WIDE>
                         const bool on = t0 + tok(i) < n && chan() < cb.count;
 #pragma unroll
                         for (int j = 0; j < NA; ++j)
-                            copy_async<4 * sizeof(T)>(to + j * TILE * CPB + i * THREADS * 4, on ? at.p[j] + i * at.rows : (const T *)a.x, on);
+                            copy_async<V * sizeof(T)>(to + j * TILE * CPB + i * THREADS * V, on ? at.p[j] + i * at.rows : (const T *)a.x, on);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < GPER; ++i) {
-                    const int e = threadIdx.x + i * THREADS, r = e % (TILE * GROW);
-                    const bool on = t0 + r / GROW < n && r % GROW * 4 < a.N;
-                    if (e < (both ? GALL : GALL / 2))
-                        copy_async<4 * sizeof(T)>(to + NA * TILE * CPB + i * THREADS * 4, on ? at.g[i] : (const T *)a.Bm, on);
+                    const Group q(i);
+                    const bool on = t0 + q.t < n && q.k < a.N;
+                    if (q.e < (both ? GALL : GALL / 2))
+                        copy_async<V * sizeof(T)>(to + NA * TILE * CPB + i * THREADS * V, on ? at.group(q) : (const T *)a.Bm, on);
                 }
                 at.move(a, step);
             }
             copies_issued();
         }
     }
-    // Access i of token array j of the tile at t0, in buffer `buf`.
+    // Access i of token array j (src) of the tile at t0, in buffer `buf`.
     __device__ __forceinline__ static void get(const T *raw, int buf, int j, int i, const SsmArgs &a, const ChannelBlock &cb, int b,
-                                               int t0, int n, const void *src, float (&f)[VEC]) {
-        const int t = tok(i), c = chan();
+                                               int t0, int n, const void *src, float (&f)[V]) {
         Vec v;
-        if constexpr (WIDE) {
-            v.load(raw + (size_t)buf * STAGE + j * TILE * CPB + (threadIdx.x + i * THREADS) * 4);
+        if constexpr (ASYNC) {
+            v.load(raw + (size_t)buf * STAGE + j * TILE * CPB + (threadIdx.x + i * THREADS) * V);
         } else {
+            const int t = tok(i), c = chan();
             v.zero();
             if (t0 + t < n && c < cb.count) v.load((const T *)src + ((size_t)b * a.T + t0 + t) * a.D + cb.first + c);
         }
         v.get(f);
     }
-    // put(which, t, k, f) for the four states from k of token t that this thread has copied (or, odd
-    // shapes, reads now): for the CTA to lay B and C out in its own way.
+    // put(which, t, k, f) for the V states from k of B (0) or C (1) of token t that this thread has
+    // copied (or reads now): for the CTA to lay B and C out in its own way.
     template <typename F>
     __device__ __forceinline__ static void get_groups(const T *raw, int buf, const SsmArgs &a, const ChannelBlock &cb, int b, int t0,
                                                       int n, bool both, F put) {
 #pragma unroll
         for (int i = 0; i < GPER; ++i) {
-            const int e = threadIdx.x + i * THREADS, which = e / (TILE * GROW), r = e % (TILE * GROW);
-            const int t = r / GROW, k = r % GROW * 4;
-            if (e >= (both ? GALL : GALL / 2)) break;
-            float f[4];
-            if constexpr (WIDE) {
-                Pack<T, 4> v;
-                v.load(raw + (size_t)buf * STAGE + NA * TILE * CPB + e * 4);
-                v.get(f);
+            const Group q(i);
+            if (q.e >= (both ? GALL : GALL / 2)) break;
+            Vec v;
+            float f[V];
+            if constexpr (ASYNC) {
+                v.load(raw + (size_t)buf * STAGE + NA * TILE * CPB + q.e * V);
             } else {
-                const T *p = groups(a, cb, b, t0 + t, which) + k;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = t0 + t < n && k + j < a.N ? to_f(p[j]) : 0.f;
+                v.zero();
+                if (t0 + q.t < n && q.k < a.N)
+                    v.load((const T *)(q.which ? a.Cm : a.Bm) + (((size_t)b * a.T + t0 + q.t) * a.G + cb.group) * a.N + q.k);
             }
-            put(which, t, k, f);
+            v.get(f);
+            put(q.which, q.t, q.k, f);
         }
     }
 };
@@ -242,14 +253,14 @@ __host__ __device__ constexpr int sum_parts(int LN) { return LN < 4 ? LN : 4; }
 // Row of the parts of y, free of bank conflicts.
 __host__ __device__ constexpr int scan_row(int LN) { return 256 / LN + (LN == 2 ? 16 : LN <= 8 ? 8 : 4); }
 
-template <typename T, int LN, bool WIDE, int MODE>
+template <typename T, int LN, int VEC, int MODE>
 __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split sp, ScanWs w) {
     constexpr int PAIRS = kScanThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
     constexpr bool OUT = MODE == kOutputs, SEG = MODE == kSegCheckpoints, CHK = SEG || MODE == kCheckpoints;
     constexpr bool BOTH = OUT || SEG;                                  // C is needed
     constexpr int PARTS = sum_parts(LN), NL = LN / PARTS, YS = scan_row(LN);
-    using St = Staging<T, kScanThreads, kTile, CPB, NP, SEG ? 3 : 2, WIDE>;
-    constexpr int VEC = St::VEC, PER = St::PER;
+    using St = Staging<T, kScanThreads, kTile, CPB, NP, SEG ? 3 : 2, VEC>;
+    constexpr int PER = St::PER;
     extern __shared__ float4 smem4[];
     T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
     float4 *su = smem4 + St::BYTES / 16;                               // [kTile][pair_row] (u0, u1, u0 x0, u1 x1)
@@ -326,7 +337,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
     int buf = 0;
     for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf = buf + 1 < kStages ? buf + 1 : 0) {
         issue(t0 + 2 * kTile, buf + 2 < kStages ? buf + 2 : buf + 2 - kStages);
-        if constexpr (WIDE) copies_done<2>();
+        if constexpr (St::ASYNC) copies_done<2>();
         const bool full = St::full(cb, t0, n);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -340,9 +351,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) u[k] = 0.f;
             }
-            if constexpr (VEC == 4) {
+            if constexpr (VEC > 1) {
 #pragma unroll
-                for (int k = 0; k < 4; k += 2)
+                for (int k = 0; k < VEC; k += 2)
                     su[t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS)] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
             } else {
                 float *to = reinterpret_cast<float *>(su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS)) + (c & 1);
@@ -356,8 +367,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                 for (int k = 0; k < VEC; ++k) sg[t * CPB + c + k] = g[k];
             }
         }
-        St::get_groups(raw, buf, a, cb, b, t0, n, BOTH, [&](int which, int t, int k, const float (&f)[4]) {
-            *reinterpret_cast<float4 *>((which ? sC : sB) + t * NP + k) = make_float4(f[0], f[1], f[2], f[3]);
+        St::get_groups(raw, buf, a, cb, b, t0, n, BOTH, [&](int which, int t, int k, const float (&f)[VEC]) {
+            Pack<float, VEC> v;
+            v.set(f);
+            v.store((which ? sC : sB) + t * NP + k);
         });
         const float4 *mine = su + pair_at(pr, PAIRS);
         __syncthreads();
@@ -414,7 +427,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
             for (int i = 0; i < PER; ++i) {
                 const int t = St::tok(i), c = St::chan();
                 if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
-                if ((PER * kScanThreads != kTile * St::ROW || !WIDE) && t >= kTile) continue;
+                if (!St::EVEN && t >= kTile) continue;
                 float f[VEC], x[VEC];
                 St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
 #pragma unroll
@@ -436,8 +449,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                 }
                 typename St::Vec o;
                 o.set(f);
-                if constexpr (WIDE) o.store(y + i * at.rows);
-                else o.store((T *)a.y + ((size_t)b * a.T + t0 + t) * D + cb.first + c);
+                o.store(y + i * at.rows);
             }
             y += (size_t)kTile * D;
         }
@@ -478,25 +490,33 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
     }
 }
 
-template <typename T, int LN, bool WIDE, int MODE>
+template <typename T, int LN, int VEC, int MODE>
 cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
     constexpr int CPB = 2 * kScanThreads / LN, NP = 4 * LN, YS = scan_row(LN);
-    using St = Staging<T, kScanThreads, kTile, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, WIDE>;
+    using St = Staging<T, kScanThreads, kTile, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, VEC>;
     const size_t smem = St::BYTES + kTile * (4 * pair_row(CPB / 2) + 2 * NP + sum_parts(LN) * YS) * sizeof(float);
-    const cudaError_t e = allow_smem(scan_kernel<T, LN, WIDE, MODE>, smem);
+    const cudaError_t e = allow_smem(scan_kernel<T, LN, VEC, MODE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
-    scan_kernel<T, LN, WIDE, MODE><<<dim3(nblk, MODE == kEnds ? sp.S - 1 : sp.S), kScanThreads, smem, s>>>(a, sp, w);
+    scan_kernel<T, LN, VEC, MODE><<<dim3(nblk, MODE == kEnds ? sp.S - 1 : sp.S), kScanThreads, smem, s>>>(a, sp, w);
     const cudaError_t r = cudaGetLastError();
     if (r == cudaSuccess) *nlaunch += 1;
     return r;
 }
 
-// Whole groups of four along a group's channels and along the states go by vector accesses.
+// Elements of an access: what divides the channels of a group and the states, and starts every
+// access on a multiple of its own size.
+template <typename T> int access_size(const SsmArgs &a) {
+    const int per = a.D / a.G;
+    return per % 4 == 0 && a.N % 4 == 0 ? 4 : sizeof(T) == 2 && per % 2 == 0 && a.N % 2 == 0 ? 2 : 1;
+}
 template <typename T, int LN, int MODE>
 cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
-    const bool wide = a.D / a.G % 4 == 0 && a.N % 4 == 0;
-    return wide ? run_scan<T, LN, true, MODE>(a, sp, w, s, nlaunch) : run_scan<T, LN, false, MODE>(a, sp, w, s, nlaunch);
+    const int v = access_size<T>(a);
+    if (v == 4) return run_scan<T, LN, 4, MODE>(a, sp, w, s, nlaunch);
+    if constexpr (sizeof(T) == 2)
+        if (v == 2) return run_scan<T, LN, 2, MODE>(a, sp, w, s, nlaunch);
+    return run_scan<T, LN, 1, MODE>(a, sp, w, s, nlaunch);
 }
 
 template <typename T, int MODE>
