@@ -23,7 +23,8 @@ struct NormPlan {
 };
 
 // LPG: the threads of a group (a power of two up to 32, or the whole CTA), or 0 where only the
-// plan knows (up to 32).
+// plan knows (up to 32).  LPG = 16 is the instance of groups that fill their lanes (128 channels in
+// bf16, 64 in fp32: the usual head): nothing has to be masked inside a group.
 template <int LPG, int CNT> __device__ __forceinline__ void group_totals(float (&v)[CNT], int lpg, float *sm) {
     const int n = LPG ? LPG : lpg;
     auto join = [&](int o) {
@@ -106,7 +107,7 @@ __device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < HV; ++i) v[k][i] = on[k] ? add2(v[k][i], pk(m, VEC == 1 ? 0.f : m)) : 0;
+            for (int i = 0; i < HV; ++i) v[k][i] = LPG == 16 || on[k] ? add2(v[k][i], pk(m, VEC == 1 ? 0.f : m)) : 0;
     }
     f32x2 q = 0;
 #pragma unroll
@@ -141,14 +142,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
     auto fetch = [&](int64_t m, size_t row) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            xn[k].zero();
-            zn[k].zero();
+            if (LPG != 16) {
+                xn[k].zero();
+                zn[k].zero();
+            }
+            // (a dead lane of a full group computes on what it has, and stores nothing)
             if (at.on[k] && m < a.M) {
                 xn[k].load((const T *)a.x + row + at.c[k]);
                 if (a.z) zn[k].load((const T *)a.z + row + at.c[k]);
             }
         }
     };
+    if (LPG == 16) {
+        xn[0].zero();
+        zn[0].zero();
+    }
     fetch(first + at.ml, row);
     // every thread of the CTA makes the same number of turns: the group totals synchronise
     for (int64_t m0 = first; m0 < a.M; m0 += turn, row += step) {
@@ -202,9 +210,11 @@ __global__ void __launch_bounds__(kNormThreads, K == 1 && LPG <= 32 ? 3 : 1) nor
     auto fetch = [&](int64_t m, size_t row) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            xn[k].zero();
-            zn[k].zero();
-            dyn[k].zero();
+            if (LPG != 16) {
+                xn[k].zero();
+                zn[k].zero();
+            }
+            dyn[k].zero();                             // (no gradient comes from a dead lane)
             if (at.on[k] && m < a.M) {
                 xn[k].load((const T *)a.x + row + at.c[k]);
                 dyn[k].load((const T *)a.dy + row + at.c[k]);
@@ -212,6 +222,10 @@ __global__ void __launch_bounds__(kNormThreads, K == 1 && LPG <= 32 ? 3 : 1) nor
             }
         }
     };
+    if (LPG == 16) {
+        xn[0].zero();
+        zn[0].zero();
+    }
     fetch(begin + at.ml, row);
     for (int64_t m0 = begin; m0 < a.M; m0 += turn, row += step) {
         const int64_t m = m0 + at.ml;
@@ -358,7 +372,7 @@ template <typename T, int VEC> void run(bool back, const NormArgs &a, const Norm
 #define QD_NORM_K(k, l) back ? run_bwd<T, VEC, k, l>(a, s.p, st) : run_fwd<T, VEC, k, l>(a, s.p, st)
     const bool whole = s.p.lpg == kNormThreads;        // a group per CTA
     if (s.K == 1 && whole) QD_NORM_K(1, kNormThreads);
-    else if (s.K == 1 && VEC > 1 && s.p.lpg == 16) QD_NORM_K(1, 16);
+    else if (s.K == 1 && VEC > 1 && a.d == 16 * VEC) QD_NORM_K(1, 16);
     else if (s.K == 1) QD_NORM_K(1, 0);
     else if (s.K == 4 && whole) QD_NORM_K(4, kNormThreads);
     else if (s.K == 4) QD_NORM_K(4, 32);

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kBatch = 4, kRing = 3;  // tokens computed together; batches in the ring
 constexpr int kFwdThreads = 128, kBwdThreads = 256, kStepThreads = 128;
-constexpr int kFwdCtas = 5, kBwdCtas = 2;    // resident on an SM
+constexpr int kFwdCtas = 4, kBwdCtas = 2;    // resident on an SM
 
 // The filters of VEC channels (w[c][j]) as pairs of channels per tap.
 template <int VEC, int W> __device__ __forceinline__ void load_filter(const float *w, f32x2 (&f)[W][(VEC + 1) / 2]) {
@@ -60,11 +60,19 @@ template <typename T, int VEC, int THREADS> struct Ahead {
     __device__ __forceinline__ static T *slot(T *ring, int buf, int u) {
         return ring + ((size_t)(buf * kBatch + u) * THREADS + threadIdx.x) * VEC;
     }
-    __device__ __forceinline__ static void issue(T *ring, int buf, const T *src, int D, int t, int end) {
+    // The batch at t, from src (its first token), and src to the next one; `any`: an address to read nothing from.
+    __device__ __forceinline__ static void issue(T *ring, int buf, const T *&src, size_t D, int t, int end, const T *any) {
         if constexpr (ASYNC) {
+            T *to = slot(ring, buf, 0);
+            if (t + kBatch <= end) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                copy_async<VEC * sizeof(T)>(slot(ring, buf, u), t + u < end ? src + (size_t)(t + u) * D : src, t + u < end);
+                for (int u = 0; u < kBatch; ++u) copy_async<VEC * sizeof(T)>(to + u * THREADS * VEC, src + u * D);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    copy_async<VEC * sizeof(T)>(to + u * THREADS * VEC, t + u < end ? src + u * D : any, t + u < end);
+            }
+            src += kBatch * D;
         }
     }
     __device__ __forceinline__ static void get(T *ring, int buf, int u, const T *src, int D, int t, int end, f32x2 (&f)[(VEC + 1) / 2]) {
@@ -99,10 +107,12 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) conv_fwd_kernel(ConvArg
     const T *x = (const T *)a.x + (size_t)b * a.T * D + c0;
     T *y = (T *)a.y + (size_t)b * a.T * D + c0;
 
-    In::issue(ring, 0, x, D, t0, end);
-    copies_issued();
-    In::issue(ring, 1, x, D, t0 + kBatch, end);
-    copies_issued();
+    const T *next = x + (size_t)t0 * D;
+#pragma unroll
+    for (int i = 0; i + 1 < kRing; ++i) {
+        In::issue(ring, i, next, D, t0 + i * kBatch, end, x);
+        copies_issued();
+    }
     f32x2 w[W][HV], bias[HV];
     load_filter<VEC, W>(a.w + (size_t)c0 * W, w);
     load_bias<VEC>(a.bias, c0, bias);
@@ -123,10 +133,11 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) conv_fwd_kernel(ConvArg
     for (int k = 0; k < W - 1; ++k) head[k].get2(win[k + 1]);
 
     int buf = 0;
+    T *yt = y + (size_t)t0 * D;
     for (int t = t0; t < t1; t += kBatch, buf = buf + 1 < kRing ? buf + 1 : 0) {
-        In::issue(ring, buf + 2 < kRing ? buf + 2 : buf + 2 - kRing, x, D, t + 2 * kBatch, end);
+        In::issue(ring, buf ? buf - 1 : kRing - 1, next, D, t + (kRing - 1) * kBatch, end, x);
         copies_issued();
-        copies_done<2>();
+        copies_done<kRing - 1>();
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
@@ -149,9 +160,10 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) conv_fwd_kernel(ConvArg
                 P out;
                 out.set2(o);
                 if (t + u >= n) out.zero();
-                out.store(y + (size_t)(t + u) * D);
+                out.store(yt + u * (size_t)D);
             }
         }
+        yt += kBatch * (size_t)D;
     }
     if (r == 0 && a.S_final) {                         // the last W - 1 inputs of S0 followed by x
 #pragma unroll
@@ -234,13 +246,14 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
     f32x2 dw[W][HV] = {}, db[HV] = {};
     if (c0 < D && (t0 < t1 || r == 0)) {
         const int stop = t1 + W - 1, end = min(stop, n);       // tokens t1 .. stop - 1 complete the run's last dx
+        const T *xn = x + (size_t)t0 * D, *gn = dy + (size_t)t0 * D;
         auto issue = [&](int t, int buf) {
-            In::issue(rx, buf, x, D, t, end);
-            In::issue(rg, buf, dy, D, t, end);
+            In::issue(rx, buf, xn, D, t, end, x);
+            In::issue(rg, buf, gn, D, t, end, dy);
             copies_issued();
         };
-        issue(t0, 0);
-        issue(t0 + kBatch, 1);
+#pragma unroll
+        for (int i = 0; i + 1 < kRing; ++i) issue(t0 + i * kBatch, i);
         f32x2 w[W][HV], bias[HV], win[W][HV], acc[W][HV] = {};
         load_filter<VEC, W>(a.w + (size_t)c0 * W, w);
         load_bias<VEC>(a.bias, c0, bias);
@@ -257,6 +270,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
             v.get2(win[k + 1]);
         }
         int buf = 0;
+        T *xs = nullptr;                                       // where the batch's first complete token goes
         // One token; INSIDE: it and its W - 1 predecessors are plain tokens of this run.
         auto token = [&](auto inside, int t, int u) {
             constexpr bool INSIDE = decltype(inside)::value;
@@ -309,7 +323,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
                 }
                 P out;
                 out.set2(o);
-                if (INSIDE || s >= 0) out.store(dx + (size_t)s * D);
+                if (INSIDE) out.store(xs + u * (size_t)D);
+                else if (s >= 0) out.store(dx + (size_t)s * D);
                 else if (a.dS0) out.store((T *)a.dS0 + ((size_t)b * (W - 1) + (s + W - 1)) * D + c0);
             }
 #pragma unroll
@@ -318,9 +333,10 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
                 for (int h = 0; h < HV; ++h) acc[j][h] = j + 1 < W ? acc[j + 1 < W ? j + 1 : j][h] : 0;
         };
         for (int t = t0; t < stop; t += kBatch, buf = buf + 1 < kRing ? buf + 1 : 0) {
-            issue(t + 2 * kBatch, buf + 2 < kRing ? buf + 2 : buf + 2 - kRing);
-            copies_done<2>();
+            issue(t + (kRing - 1) * kBatch, buf ? buf - 1 : kRing - 1);
+            copies_done<kRing - 1>();
             if (t >= t0 + W - 1 && t + kBatch <= min(t1, n)) {
+                xs = dx + (size_t)(t - (W - 1)) * D;
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) token(std::true_type{}, t, u);
             } else {

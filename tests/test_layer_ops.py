@@ -549,3 +549,48 @@ def test_sequences_of_no_tokens(qd):
     assert not qd.ssm_bwd(x, x, A, BC, BC, None, None, None, x)["dA"].any()
     n = torch.zeros(0, 2, 8, device="cuda")
     assert not qd.group_norm_bwd(n, torch.ones(2, 8, device="cuda"), None, None, n)["dw"].any()
+
+
+# ------------------------------------------------------------------ offsets beyond 32 bits
+
+@pytest.mark.gpu
+def test_arrays_of_more_than_two_to_the_31_elements(qd):
+    """The tail of a very long sequence is that of a short one that starts from its state."""
+    T, D, N, tail = (1 << 20) + 37, 2056, 16, 45
+    assert T * D > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x = torch.empty(1, T, D, dtype=BF16, device="cuda").normal_(generator=g)
+    w, bias = 0.5 * r(D, 4), 0.1 * r(D)
+    cut = lambda t: t[:, T - tail:].contiguous()
+    half = lambda a, b: (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()   # one bf16 ulp
+
+    y, S = qd.short_conv_fwd(x, w, bias)
+    before = x[:, T - tail - 3:T - tail].contiguous()
+    y2, S2 = qd.short_conv_fwd(cut(x), w, bias, before)
+    assert torch.equal(cut(y), y2) and torch.equal(S, S2)
+    gx = qd.short_conv_bwd(x, w, bias, None, y)["dx"]
+    g2 = qd.short_conv_bwd(cut(x), w, bias, before, cut(y))["dx"]
+    assert torch.equal(cut(gx), g2)
+    del gx
+
+    n = qd.group_norm_fwd(x.view(T, 8, 257))
+    assert torch.equal(n[T - tail:], qd.group_norm_fwd(x.view(T, 8, 257)[T - tail:].contiguous()))
+    gn = qd.group_norm_bwd(x.view(T, 8, 257), None, None, None, n)["dx"]
+    want = qd.group_norm_bwd(x.view(T, 8, 257)[T - tail:].contiguous(), None, None, None, n[T - tail:].contiguous())["dx"]
+    assert torch.equal(gn[T - tail:], want)
+    del n, gn
+
+    delta = y
+    A, skip, db = -(1 + torch.arange(N, device="cuda").float()).repeat(D, 1), torch.ones(D, device="cuda"), -3 + r(D)
+    B, C = r(1, T, 1, N).to(BF16), r(1, T, 1, N).to(BF16)
+    args = lambda f, S0=None: (f(x), f(delta), A, f(B), f(C), skip, db, S0)
+    ys, Ss = qd.ssm_fwd(*args(lambda t: t))
+    _, mid = qd.ssm_fwd(*args(lambda t: t[:, :T - tail].contiguous()))
+    y3, S3 = qd.ssm_fwd(*args(cut, mid))
+    assert half(cut(ys), y3)
+    assert (Ss - S3).norm() <= 1e-5 * S3.norm()
+    gs = qd.ssm_bwd(*args(lambda t: t), x)
+    g3 = qd.ssm_bwd(*args(cut, mid), cut(x))
+    for k in ("dx", "ddelta", "dB", "dC"):
+        assert half(cut(gs[k]), g3[k]), k
