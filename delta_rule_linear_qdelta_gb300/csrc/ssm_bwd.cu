@@ -27,6 +27,7 @@ namespace {
 
 using namespace ssm;
 
+constexpr int kStages = 3;
 constexpr int kGradThreads = 128, kGradWarps = kGradThreads / 32, kSumThreads = 256;
 
 // Everything in the workspace, in floats from its start.
@@ -47,7 +48,7 @@ BwdWs bwd_ws(int B, int T, int D, int G, int N) {
     // One segment when the CTAs fill every SM's three places; otherwise two rounds of them: one
     // round is 3 % faster at equal lengths, two are 17 % faster at ragged ones (4 x 4096 x 1024 and
     // 3 x 517 x 770 channels).
-    w.sp = split_tokens((int64_t)B * G * w.nb, T, 3 * kSMs, 6 * kSMs, 4 * kTile);
+    w.sp = split_tokens((int64_t)B * G * w.nb, T, 3 * kSMs, 6 * kSMs, 8 * kChunk, kChunk);
     w.nck = (T + kChunk - 1) / kChunk;
     w.rows = B * w.sp.S;
     const bool multi = w.sp.S > 1;
@@ -80,7 +81,7 @@ template <typename T, int LN, int VEC>
 __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN, CL = 32 / LN;
     constexpr int PARTS = sum_parts(LN), NL = LN / PARTS, PR = part_row(LN);
-    using St = Staging<T, kGradThreads, kChunk, CPB, NP, 3, VEC>;
+    using St = Staging<T, kGradThreads, kChunk, CPB, NP, 3, VEC, kStages>;
     constexpr int PER = St::PER;
     extern __shared__ float4 smem4[];
     T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] chunks on their way
@@ -492,7 +493,7 @@ template <typename T> __global__ void __launch_bounds__(kSumThreads) groups_kern
 
 template <typename T, int LN, int VEC> cudaError_t run_grads(const SsmArgs &a, const BwdWs &w, cudaStream_t s) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
-    const size_t smem = Staging<T, kGradThreads, kChunk, CPB, NP, 3, VEC>::BYTES +
+    const size_t smem = Staging<T, kGradThreads, kChunk, CPB, NP, 3, VEC, kStages>::BYTES +
                         kChunk * (4 * pair_row(PAIRS) + 4 * sum_parts(LN) * part_row(LN) + 2 * PAIRS + CPB + kGradWarps * 2 * NP) * sizeof(float) +
                         8 * order_size(NP) * sizeof(float);
     const cudaError_t e = allow_smem(grads_kernel<T, LN, VEC>, smem);

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmArgs a, int per_g
 // whole, 293 and 316 us in four and two segments, bf16); otherwise enough for four CTAs per SM
 // (32 CTAs of 1 x 32768 x 2048: 578 us, 633 us at three).
 Split fwd_split(int B, int T, int D, int G, int N) {
-    return split_tokens(scan_ctas(B, D, G, N), T, kSMs, 4 * kSMs, 4 * kTile);
+    return split_tokens(scan_ctas(B, D, G, N), T, kSMs, 4 * kSMs, 4 * kTile, kTile);
 }
 
 template <typename T> cudaError_t run_fwd(const SsmArgs &a, cudaStream_t s, int *nlaunch) {

@@ -14,9 +14,12 @@
 // the warps, which the recurrence needs to cover its latencies.  (bf16 B and C kept as they come
 // halve the reads, but unpacking them at every use costs more: 557 -> 602 us, 32768 tokens.)
 // A CTA of four warps takes CPB = 256 / LN channels of one sequence and walks its tokens in tiles
-// of 16, staged in shared memory as fp32 (softplus once per token and channel) while the next
-// two tiles are on their way.  y goes back through shared memory, so rows are written as they
-// are read.
+// staged in shared memory as fp32 (softplus once per token and channel) while the next ones are
+// on their way: tiles of 16, and y goes back through shared memory, so rows are written as they
+// are read.  The backward's checkpoints take tiles of 8 in two halves: between two barriers a warp
+// stages the next tile and computes the one at hand, and warps drift apart in what they do.
+// (With outputs that costs, for what is done once a tile then counts twice: 227 -> 246 us at
+// 8 x 2048 x 2048 x 16 in bf16.)
 #pragma once
 
 #include "layer_common.cuh"
@@ -26,7 +29,7 @@ namespace ssm {
 
 constexpr int kScanThreads = 128;
 constexpr int kTile = 16;             // tokens staged at a time
-constexpr int kChunk = 8;             // tokens between the backward's checkpoints
+constexpr int kChunk = 8;             // tokens between the backward's checkpoints, which are staged at a time there
 
 __host__ __device__ constexpr int padded_states(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128; }
 
@@ -44,18 +47,18 @@ struct ChannelBlock {
     }
 };
 
-// Tokens cut into S segments of `len` (a multiple of the tile): one when `ctas` CTAs already
-// number `enough`, else about `want` CTAs in all, of at least `least` tokens.
+// Tokens cut into S segments of `len` (a multiple of `align`, the tile): one when `ctas` CTAs
+// already number `enough`, else about `want` CTAs in all, of at least `least` tokens.
 struct Split {
     int S, len;
 };
-inline Split split_tokens(int64_t ctas, int T, int64_t enough, int64_t want, int least) {
+inline Split split_tokens(int64_t ctas, int T, int64_t enough, int64_t want, int least, int align) {
     Split s{1, T > 0 ? T : 1};
     if (ctas <= 0 || ctas >= enough) return s;
     int64_t S = want / ctas, most = T / least;
     if (S > most) S = most;
     if (S < 2) return s;
-    s.len = (int)(((T + S - 1) / S + kTile - 1) / kTile * kTile);
+    s.len = (int)(((T + S - 1) / S + align - 1) / align * align);
     s.S = (T + s.len - 1) / s.len;
     return s;
 }
@@ -87,14 +90,12 @@ template <int VEC> __device__ __forceinline__ void step_sizes(float (&u)[VEC], c
 }
 
 // A tile of TILE tokens on its way from global to shared memory: NA token arrays and B and C.  The raw
-// tile arrives by asynchronous copies, two tiles ahead, in one of kStages buffers; every thread
+// tile arrives by asynchronous copies, some tiles ahead, in one of STAGES buffers; every thread
 // then reads back what it copied itself (so its own wait is enough), converts it and stages it
 // for the CTA.  An access is V neighbouring channels of a token, or V states of its B or C: 4, or for
 // odd shapes 2 (bf16) or 1; single bf16 values are below what a copy can move and are read when they
 // are staged.  What is beyond the sequence, the block's channels or N arrives as zero.
-constexpr int kStages = 3;
-
-template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, int V> struct Staging {
+template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, int V, int STAGES> struct Staging {
     static constexpr bool ASYNC = V * sizeof(T) >= 4;
     static constexpr int ROW = CPB / V;                                // accesses a token
     static constexpr int PER = (TILE * ROW + THREADS - 1) / THREADS;
@@ -103,7 +104,7 @@ template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, int V> str
     static constexpr int GPER = (GALL + THREADS - 1) / THREADS;
     static_assert(THREADS % ROW == 0);                                 // a thread's channels are the same every time
     static constexpr int STAGE = ASYNC ? (NA * TILE * CPB + 2 * TILE * NP) : 0;    // elements of a raw tile
-    static constexpr size_t BYTES = (size_t)kStages * STAGE * sizeof(T);
+    static constexpr size_t BYTES = (size_t)STAGES * STAGE * sizeof(T);
     using Vec = Pack<T, V>;
 
     __device__ __forceinline__ static int tok(int i) { return (threadIdx.x + i * THREADS) / ROW; }
@@ -253,21 +254,35 @@ __host__ __device__ constexpr int sum_parts(int LN) { return LN < 4 ? LN : 4; }
 // Row of the parts of y, free of bank conflicts.
 __host__ __device__ constexpr int scan_row(int LN) { return 256 / LN + (LN == 2 ? 16 : LN <= 8 ? 8 : 4); }
 
+// Tiles and shared memory of a mode.
+template <typename T, int LN, int VEC, int MODE> struct ScanSize {
+    static constexpr bool OUT = MODE == kOutputs, SEG = MODE == kSegCheckpoints;
+    static constexpr int PAIRS = kScanThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
+    static constexpr bool DRIFT = SEG || MODE == kCheckpoints;
+    static constexpr int TILE = DRIFT ? kChunk : kTile, HALVES = DRIFT ? 2 : 1;
+    static constexpr int AHEAD = DRIFT ? 3 : sizeof(T) == 4 ? 1 : 2;   // tiles on their way (fp32: as many as leave room for four CTAs)
+    static constexpr int STAGES = AHEAD + 1;
+    using St = Staging<T, kScanThreads, TILE, CPB, NP, SEG ? 3 : 2, VEC, STAGES>;
+    static constexpr int SU = TILE * pair_row(PAIRS);                  // float4
+    static constexpr int SG = TILE * NP * (OUT || SEG ? 2 : 1);        // floats, as below
+    static constexpr int SY = OUT ? TILE * sum_parts(LN) * scan_row(LN) : SEG ? TILE * CPB : 0;
+    static constexpr size_t BYTES = St::BYTES + HALVES * (SU * 4 + SG + SY) * sizeof(float);
+};
+
 template <typename T, int LN, int VEC, int MODE>
 __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split sp, ScanWs w) {
     constexpr int PAIRS = kScanThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN;
     constexpr bool OUT = MODE == kOutputs, SEG = MODE == kSegCheckpoints, CHK = SEG || MODE == kCheckpoints;
     constexpr bool BOTH = OUT || SEG;                                  // C is needed
     constexpr int PARTS = sum_parts(LN), NL = LN / PARTS, YS = scan_row(LN);
-    using St = Staging<T, kScanThreads, kTile, CPB, NP, SEG ? 3 : 2, VEC>;
-    constexpr int PER = St::PER;
+    using Z = ScanSize<T, LN, VEC, MODE>;
+    using St = typename Z::St;
+    constexpr int TILE = Z::TILE, AHEAD = Z::AHEAD, STAGES = Z::STAGES, PER = St::PER, SU = Z::SU, SG = Z::SG, SY = Z::SY;
     extern __shared__ float4 smem4[];
-    T *raw = reinterpret_cast<T *>(smem4);                             // [kStages] tiles on their way
-    float4 *su = smem4 + St::BYTES / 16;                               // [kTile][pair_row] (u0, u1, u0 x0, u1 x1)
-    float *sB = reinterpret_cast<float *>(su + kTile * pair_row(PAIRS));  // [kTile][NP]
-    float *sC = sB + kTile * NP;                                       // [kTile][NP]         BOTH
-    float *sy = sC + kTile * NP;                                       // [kTile][PARTS][YS] y OUT
-    float *sg = sy;                                                    // [kTile][CPB] dy     SEG
+    T *raw = reinterpret_cast<T *>(smem4);                             // [STAGES] tiles on their way
+    float4 *su = smem4 + St::BYTES / 16;                               // [HALVES][TILE][pair_row] (u0, u1, u0 x0, u1 x1)
+    float *sB = reinterpret_cast<float *>(su + Z::HALVES * SU);        // [HALVES] B and (BOTH) C, [TILE][NP] each
+    float *sy = sB + Z::HALVES * SG;                                   // [HALVES] OUT: parts of y, [TILE][PARTS][YS]; SEG: dy, [TILE][CPB]
 
     const int lane = threadIdx.x & 31, ln = threadIdx.x % LN, pr = threadIdx.x / LN, seg = blockIdx.y;
     const int nblk = channel_blocks(a.D, a.G, CPB), b = blockIdx.x / nblk;
@@ -329,133 +344,165 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         else return typename St::Cursor(a, cb, b, t_begin, {a.x, a.delta});
     };
     typename St::Cursor at = cursor();
-    auto issue = [&](int t0, int buf) { St::issue(at, raw, buf, a, cb, t0, t0 < t_end, n, BOTH, 1); };
     T *y = OUT ? (T *)a.y + ((size_t)b * a.T + t_begin + St::tok(0)) * D + cb.first + St::chan() : nullptr;
     f32x2 U = 0;                                                       // of the two channels
-    issue(t_begin, 0);
-    issue(t_begin + kTile, 1);
-    int buf = 0;
-    for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf = buf + 1 < kStages ? buf + 1 : 0) {
-        issue(t0 + 2 * kTile, buf + 2 < kStages ? buf + 2 : buf + 2 - kStages);
-        if constexpr (St::ASYNC) copies_done<2>();
+
+    auto issue = [&](int t0, int slot) { St::issue(at, raw, slot, a, cb, t0, t0 < t_end, n, BOTH, 1); };
+    // the tile at t0, arrived in `slot`, to half `half` of the staging arrays
+    auto stage = [&](int t0, int slot, int half) {
         const bool full = St::full(cb, t0, n);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int t = St::tok(i), c = St::chan();
-            if (t >= kTile) break;
+            if (!St::EVEN && t >= TILE) break;
             float u[VEC], x[VEC];
-            St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
-            St::get(raw, buf, 1, i, a, cb, b, t0, n, a.delta, u);
+            St::get(raw, slot, 0, i, a, cb, b, t0, n, a.x, x);
+            St::get(raw, slot, 1, i, a, cb, b, t0, n, a.delta, u);
             step_sizes<VEC>(u, bias, a.softplus);
             if (!full && !(t0 + t < n && c < cb.count)) {              // of the padding nothing counts
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) u[k] = 0.f;
             }
+            float4 *row = su + half * SU + t * pair_row(PAIRS);
             if constexpr (VEC > 1) {
 #pragma unroll
                 for (int k = 0; k < VEC; k += 2)
-                    su[t * pair_row(PAIRS) + pair_at((c + k) / 2, PAIRS)] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
+                    row[pair_at((c + k) / 2, PAIRS)] = make_float4(u[k], u[k + 1], u[k] * x[k], u[k + 1] * x[k + 1]);
             } else {
-                float *to = reinterpret_cast<float *>(su + t * pair_row(PAIRS) + pair_at(c / 2, PAIRS)) + (c & 1);
+                float *to = reinterpret_cast<float *>(row + pair_at(c / 2, PAIRS)) + (c & 1);
                 to[0] = u[0];
                 to[2] = u[0] * x[0];
             }
             if constexpr (SEG) {
                 float g[VEC];
-                St::get(raw, buf, 2, i, a, cb, b, t0, n, a.dy, g);
+                St::get(raw, slot, 2, i, a, cb, b, t0, n, a.dy, g);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) sg[t * CPB + c + k] = g[k];
+                for (int k = 0; k < VEC; ++k) sy[half * SY + t * CPB + c + k] = g[k];
             }
         }
-        St::get_groups(raw, buf, a, cb, b, t0, n, BOTH, [&](int which, int t, int k, const float (&f)[VEC]) {
+        St::get_groups(raw, slot, a, cb, b, t0, n, BOTH, [&](int which, int t, int k, const float (&f)[VEC]) {
             Pack<float, VEC> v;
             v.set(f);
-            v.store((which ? sC : sB) + t * NP + k);
+            v.store(sB + half * SG + (which * TILE + t) * NP + k);
         });
-        const float4 *mine = su + pair_at(pr, PAIRS);
-        __syncthreads();
-#pragma unroll 1
-        for (int tc = 0; tc < kTile; tc += kChunk) {
-            if (CHK && t0 + tc < t_end) {
-                const size_t row = (size_t)((t0 + tc) / kChunk) * all + bd;
-                put_state(w.chk, row, 0, h[0]);
-                put_state(w.chk, row, 1, h[1]);
-                if (SEG && ln == 0) {
-                    float u0, u1;
-                    unpk(U, u0, u1);
-                    if (c0 < cb.count) w.ucum[row] = u0;
-                    if (c0 + 1 < cb.count) w.ucum[row + 1] = u1;
-                }
+    };
+    // the rows of y of the tile at t0 and the next place in y
+    auto finish = [&](int t0, int slot, int half) {
+        const bool full = St::full(cb, t0, n);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = St::tok(i), c = St::chan();
+            if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
+            if (!St::EVEN && t >= TILE) continue;
+            float f[VEC], x[VEC];
+            St::get(raw, slot, 0, i, a, cb, b, t0, n, a.x, x);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                Pack<float, VEC> part;
+                float g[VEC];
+                part.load(sy + half * SY + (t * PARTS + q) * YS + c);
+                part.get(g);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) f[k] = q ? f[k] + g[k] : g[k];
             }
+            if (a.Dskip) {
 #pragma unroll
-            for (int k = 0; k < kChunk; ++k) {
-                const int t = tc + k;
-                const float4 q = mine[t * pair_row(PAIRS)];
-                const ulonglong2 Bq = *reinterpret_cast<const ulonglong2 *>(sB + t * NP + ln * 4);
-                const ulonglong2 Cq = BOTH ? *reinterpret_cast<const ulonglong2 *>(sC + t * NP + ln * 4) : ulonglong2{};
-                const f32x2 Bv[2] = {Bq.x, Bq.y}, Cv[2] = {Cq.x, Cq.y};
-                float v[2];
-                if (MODE == kEnds || SEG) U = add2(U, pk(q.x, q.y));
-                const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
+                for (int k = 0; k < VEC; ++k) f[k] = fmaf(skip[k], x[k], f[k]);
+            }
+            if (!full && t0 + t >= n) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    f32x2 acc = 0;
-                    const float g = SEG ? sg[t * CPB + c0 + c] : 0.f;
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const f32x2 av = decay2(uu[c], A2[c][p]);
-                        h[c][p] = fma2(av, h[c][p], mul2(ux[c], Bv[p]));
-                        if (OUT) acc = p ? fma2(Cv[p], h[c][p], acc) : mul2(Cv[p], h[c][p]);
-                        if (SEG) {
-                            P[c][p] = mul2(P[c][p], av);
-                            R[c][p] = fma2(P[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
-                        }
-                    }
-                    if (OUT) v[c] = sum2(acc);
-                }
-                if (OUT) {
-                    lane_reduce<2, NL, PARTS>(v, lane);
-                    float *to = sy + (t * PARTS + ln % PARTS) * YS + c0;
-                    if constexpr (NL == 1) *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
-                    else if (reduced_owner<2, NL, PARTS>(lane)) to[reduced_first<2, NL, PARTS>(lane)] = v[0];
-                }
+                for (int k = 0; k < VEC; ++k) f[k] = 0.f;
+            }
+            typename St::Vec o;
+            o.set(f);
+            o.store(y + i * at.rows);
+        }
+        y += (size_t)TILE * D;
+    };
+
+    // the kChunk tokens from `from` on of the staged tile, the first of them token tc
+    auto compute = [&](int tc, int from, int half) {
+        if (CHK) {                                                     // tc is a checkpoint of the segment
+            const size_t row = (size_t)(tc / kChunk) * all + bd;
+            put_state(w.chk, row, 0, h[0]);
+            put_state(w.chk, row, 1, h[1]);
+            if (SEG && ln == 0) {
+                float u0, u1;
+                unpk(U, u0, u1);
+                if (c0 < cb.count) w.ucum[row] = u0;
+                if (c0 + 1 < cb.count) w.ucum[row + 1] = u1;
             }
         }
-        __syncthreads();
-        if constexpr (OUT) {
+        const float4 *mine = su + half * SU + from * pair_row(PAIRS) + pair_at(pr, PAIRS);
+        const float *gB = sB + half * SG + from * NP + ln * 4, *gC = gB + TILE * NP;
+        float *part = sy + half * SY + (from * PARTS + ln % PARTS) * YS + c0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int t = St::tok(i), c = St::chan();
-                if (!full && (t0 + t >= t_stop || c >= cb.count)) continue;
-                if (!St::EVEN && t >= kTile) continue;
-                float f[VEC], x[VEC];
-                St::get(raw, buf, 0, i, a, cb, b, t0, n, a.x, x);
+        for (int t = 0; t < kChunk; ++t) {
+            const float4 q = mine[t * pair_row(PAIRS)];
+            const ulonglong2 Bq = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
+            const ulonglong2 Cq = BOTH ? *reinterpret_cast<const ulonglong2 *>(gC + t * NP) : ulonglong2{};
+            const f32x2 Bv[2] = {Bq.x, Bq.y}, Cv[2] = {Cq.x, Cq.y};
+            float v[2];
+            if (MODE == kEnds || SEG) U = add2(U, pk(q.x, q.y));
+            const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
 #pragma unroll
-                for (int q = 0; q < PARTS; ++q) {
-                    Pack<float, VEC> part;
-                    float g[VEC];
-                    part.load(sy + (t * PARTS + q) * YS + c);
-                    part.get(g);
+            for (int c = 0; c < 2; ++c) {
+                f32x2 acc = 0;
+                const float g = SEG ? sy[half * SY + (from + t) * CPB + c0 + c] : 0.f;
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) f[k] = q ? f[k] + g[k] : g[k];
+                for (int p = 0; p < 2; ++p) {
+                    const f32x2 av = decay2(uu[c], A2[c][p]);
+                    h[c][p] = fma2(av, h[c][p], mul2(ux[c], Bv[p]));
+                    if (OUT) acc = p ? fma2(Cv[p], h[c][p], acc) : mul2(Cv[p], h[c][p]);
+                    if (SEG) {
+                        P[c][p] = mul2(P[c][p], av);
+                        R[c][p] = fma2(P[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
+                    }
                 }
-                if (a.Dskip) {
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) f[k] = fmaf(skip[k], x[k], f[k]);
-                }
-                if (!full && t0 + t >= n) {
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) f[k] = 0.f;
-                }
-                typename St::Vec o;
-                o.set(f);
-                o.store(y + i * at.rows);
+                if (OUT) v[c] = sum2(acc);
             }
-            y += (size_t)kTile * D;
+            if (OUT) {
+                lane_reduce<2, NL, PARTS>(v, lane);
+                if constexpr (NL == 1) *reinterpret_cast<float2 *>(part + t * PARTS * YS) = make_float2(v[0], v[1]);
+                else if (reduced_owner<2, NL, PARTS>(lane)) part[t * PARTS * YS + reduced_first<2, NL, PARTS>(lane)] = v[0];
+            }
+        }
+    };
+
+    auto later = [](int slot, int by) { return slot + by < STAGES ? slot + by : slot + by - STAGES; };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) issue(t_begin + i * TILE, i);
+    int slot = 0;                                                      // of the tile at hand
+    if constexpr (!Z::DRIFT) {
+        for (int t0 = t_begin; t0 < t_end; t0 += TILE, slot = later(slot, 1)) {
+            issue(t0 + AHEAD * TILE, later(slot, AHEAD));
+            if constexpr (St::ASYNC) copies_done<AHEAD>();
+            stage(t0, slot, 0);
+            __syncthreads();
+#pragma unroll 1
+            for (int from = 0; from < TILE; from += kChunk) compute(t0 + from, from, 0);
+            __syncthreads();
+            if (OUT) finish(t0, slot, 0);
+        }
+    } else {
+        if (t_begin < t_end) {
+            if constexpr (St::ASYNC) copies_done<AHEAD - 1>();
+            stage(t_begin, 0, 0);
+        }
+        __syncthreads();
+        int half = 0;
+        for (int t0 = t_begin; t0 < t_end; t0 += TILE, slot = later(slot, 1), half ^= 1) {
+            issue(t0 + AHEAD * TILE, later(slot, AHEAD));
+            if (t0 + TILE < t_end) {
+                if constexpr (St::ASYNC) copies_done<AHEAD - 1>();
+                stage(t0 + TILE, later(slot, 1), half ^ 1);
+            }
+            compute(t0, 0, half);
+            __syncthreads();
         }
     }
     if constexpr (OUT) {                                               // whole tiles of padding
-        const int done = t_begin < t_end ? t_begin + (t_end - t_begin + kTile - 1) / kTile * kTile : t_begin;
+        const int done = t_begin < t_end ? t_begin + (t_end - t_begin + TILE - 1) / TILE * TILE : t_begin;
         for (int64_t e = threadIdx.x; e < (int64_t)max(t_stop - done, 0) * cb.count; e += kScanThreads)
             ((T *)a.y)[((size_t)b * a.T + done + e / cb.count) * D + cb.first + e % cb.count] = from_f<T>(0.f);
     }
@@ -492,9 +539,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
 
 template <typename T, int LN, int VEC, int MODE>
 cudaError_t run_scan(const SsmArgs &a, const Split &sp, const ScanWs &w, cudaStream_t s, int *nlaunch) {
-    constexpr int CPB = 2 * kScanThreads / LN, NP = 4 * LN, YS = scan_row(LN);
-    using St = Staging<T, kScanThreads, kTile, CPB, NP, MODE == kSegCheckpoints ? 3 : 2, VEC>;
-    const size_t smem = St::BYTES + kTile * (4 * pair_row(CPB / 2) + 2 * NP + sum_parts(LN) * YS) * sizeof(float);
+    constexpr int CPB = 2 * kScanThreads / LN;
+    constexpr size_t smem = ScanSize<T, LN, VEC, MODE>::BYTES;
     const cudaError_t e = allow_smem(scan_kernel<T, LN, VEC, MODE>, smem);
     if (e != cudaSuccess) return e;
     const unsigned nblk = (unsigned)(a.B * channel_blocks(a.D, a.G, CPB));
