@@ -75,17 +75,18 @@ template <int VEC, int K> struct Place {
     __device__ __forceinline__ void param(const float *p, int d, float none, f32x2 (&f)[K][(VEC + 1) / 2]) const {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            Pack<float, VEC < 4 ? VEC : 4> q[VEC < 4 ? 1 : VEC / 4];
+            constexpr int Q = VEC < 4 ? VEC : 4, H = (Q + 1) / 2;      // floats of an access, pairs of it
 #pragma unroll
             for (int i = 0; i < (VEC + 1) / 2; ++i) f[k][i] = both(none);
             if (p && on[k]) {
 #pragma unroll
-                for (int i = 0; i < (VEC < 4 ? 1 : VEC / 4); ++i) {
-                    q[i].load(p + (size_t)h * d + c[k] + 4 * i);
-                    f32x2 g[VEC < 4 ? 1 : 2];
-                    q[i].get2(g);
+                for (int i = 0; i < VEC / Q; ++i) {
+                    Pack<float, Q> q;
+                    f32x2 g[H];
+                    q.load(p + (size_t)h * d + c[k] + Q * i);
+                    q.get2(g);
 #pragma unroll
-                    for (int j = 0; j < (VEC < 4 ? 1 : 2); ++j) f[k][2 * i + j] = g[j];
+                    for (int j = 0; j < H; ++j) f[k][H * i + j] = g[j];
                 }
             }
         }
@@ -337,7 +338,7 @@ struct NormShape {
 NormShape norm_shape(int M, int H, int d, int dtype, int ctas_per_sm) {
     NormShape s;
     const int wide = dtype == kBF16 ? 8 : 4;
-    s.vec = d % wide == 0 ? wide : 1;
+    s.vec = d % wide == 0 ? wide : d % 2 == 0 ? 2 : 1;
     const int nv = d / s.vec;
     if (nv <= 32) {
         s.p.lpg = 1;
@@ -348,7 +349,7 @@ NormShape norm_shape(int M, int H, int d, int dtype, int ctas_per_sm) {
         s.K = nv <= 64 && s.vec > 1 ? 2 : 4;
     } else {
         s.p.lpg = kNormThreads;
-        s.K = nv <= kNormThreads && s.vec > 1 ? 1 : nv <= 4 * kNormThreads ? 4 : s.vec > 1 ? 8 : 32;
+        s.K = nv <= kNormThreads && s.vec > 1 ? 1 : nv <= 4 * kNormThreads ? 4 : s.vec == 4 ? 8 : s.vec == 2 ? 16 : 32;
     }
     const int slots = kNormThreads / s.p.lpg;
     s.p.HB = H < slots ? H : slots;
@@ -372,22 +373,25 @@ template <typename T, int VEC> void run(bool back, const NormArgs &a, const Norm
 #define QD_NORM_K(k, l) back ? run_bwd<T, VEC, k, l>(a, s.p, st) : run_fwd<T, VEC, k, l>(a, s.p, st)
     const bool whole = s.p.lpg == kNormThreads;        // a group per CTA
     if (s.K == 1 && whole) QD_NORM_K(1, kNormThreads);
-    else if (s.K == 1 && VEC > 1 && a.d == 16 * VEC) QD_NORM_K(1, 16);
+    else if (s.K == 1 && VEC > 2 && a.d == 16 * VEC) QD_NORM_K(1, 16);
     else if (s.K == 1) QD_NORM_K(1, 0);
     else if (s.K == 4 && whole) QD_NORM_K(4, kNormThreads);
     else if (s.K == 4) QD_NORM_K(4, 32);
     else if constexpr (VEC == 1) QD_NORM_K(32, kNormThreads);
     else if (s.K == 2) QD_NORM_K(2, 32);
     else if constexpr (VEC == 4) QD_NORM_K(8, kNormThreads);
+    else if constexpr (VEC == 2) QD_NORM_K(16, kNormThreads);
 #undef QD_NORM_K
 }
 
 cudaError_t launch(bool back, const NormArgs &a, const NormShape &s, int dtype, cudaStream_t st, int *nlaunch) {
     if (dtype == kBF16) {
         if (s.vec == 8) run<__nv_bfloat16, 8>(back, a, s, st);
+        else if (s.vec == 2) run<__nv_bfloat16, 2>(back, a, s, st);
         else run<__nv_bfloat16, 1>(back, a, s, st);
     } else {
         if (s.vec == 4) run<float, 4>(back, a, s, st);
+        else if (s.vec == 2) run<float, 2>(back, a, s, st);
         else run<float, 1>(back, a, s, st);
     }
     const cudaError_t e = cudaGetLastError();

@@ -23,7 +23,13 @@ constexpr int kFwdCtas = 4, kBwdCtas = 2;    // resident on an SM
 // The filters of VEC channels (w[c][j]) as pairs of channels per tap.
 template <int VEC, int W> __device__ __forceinline__ void load_filter(const float *w, f32x2 (&f)[W][(VEC + 1) / 2]) {
     float flat[(VEC + 1) * W];
-    if constexpr (VEC > 1) {
+    if constexpr (VEC == 2) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float2 v = reinterpret_cast<const float2 *>(w)[i];
+            flat[2 * i] = v.x; flat[2 * i + 1] = v.y;
+        }
+    } else if constexpr (VEC > 2) {
 #pragma unroll
         for (int i = 0; i < VEC * W / 4; ++i) {
             const float4 v = reinterpret_cast<const float4 *>(w)[i];
@@ -52,7 +58,7 @@ __device__ __forceinline__ int seq_len(const int *lens, int b, int T) {
 }
 
 // One array's tokens ahead: slot u of batch i of this thread's ring, or zeros past `end`.  Single
-// 16-bit elements are below what a copy can move and are loaded when they are used.
+// 16-bit elements are below what a copy can move.
 template <typename T, int VEC, int THREADS> struct Ahead {
     using P = Pack<T, VEC>;
     static constexpr bool ASYNC = VEC * sizeof(T) >= 4;
@@ -75,14 +81,20 @@ template <typename T, int VEC, int THREADS> struct Ahead {
             src += kBatch * D;
         }
     }
-    __device__ __forceinline__ static void get(T *ring, int buf, int u, const T *src, int D, int t, int end, f32x2 (&f)[(VEC + 1) / 2]) {
-        P v;
-        if constexpr (ASYNC) {
-            v.load(slot(ring, buf, u));
-        } else {
-            v.zero();
-            if (t + u < end) v.load(src + (size_t)(t + u) * D);
+    // What cannot be copied is loaded a batch at a time instead.
+    __device__ __forceinline__ static void arrive(P (&now)[kBatch], const T *src, int D, int t, int end) {
+        if constexpr (!ASYNC) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                now[u].zero();
+                if (t + u < end) now[u].load(src + (size_t)(t + u) * D);
+            }
         }
+    }
+    __device__ __forceinline__ static void get(T *ring, int buf, int u, const P (&now)[kBatch], f32x2 (&f)[(VEC + 1) / 2]) {
+        P v;
+        if constexpr (ASYNC) v.load(slot(ring, buf, u));
+        else v = now[u];
         v.get2(f);
     }
 };
@@ -138,13 +150,15 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) conv_fwd_kernel(ConvArg
         In::issue(ring, buf ? buf - 1 : kRing - 1, next, D, t + (kRing - 1) * kBatch, end, x);
         copies_issued();
         copies_done<kRing - 1>();
+        P now[kBatch];
+        In::arrive(now, x, D, t, end);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
 #pragma unroll
                 for (int h = 0; h < HV; ++h) win[k][h] = win[k + 1][h];
-            In::get(ring, buf, u, x, D, t, end, win[W - 1]);
+            In::get(ring, buf, u, now, win[W - 1]);
             f32x2 o[HV];
 #pragma unroll
             for (int h = 0; h < HV; ++h) {
@@ -271,6 +285,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
         }
         int buf = 0;
         T *xs = nullptr;                                       // where the batch's first complete token goes
+        P xnow[kBatch], gnow[kBatch];
         // One token; INSIDE: it and its W - 1 predecessors are plain tokens of this run.
         auto token = [&](auto inside, int t, int u) {
             constexpr bool INSIDE = decltype(inside)::value;
@@ -280,8 +295,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
             for (int k = 0; k < W - 1; ++k)
 #pragma unroll
                 for (int h = 0; h < HV; ++h) win[k][h] = win[k + 1][h];
-            In::get(rx, buf, u, x, D, t, end, win[W - 1]);
-            In::get(rg, buf, u, dy, D, t, end, g);
+            In::get(rx, buf, u, xnow, win[W - 1]);
+            In::get(rg, buf, u, gnow, g);
             if (a.silu) {
 #pragma unroll
                 for (int h = 0; h < HV; ++h) {
@@ -335,6 +350,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
         for (int t = t0; t < stop; t += kBatch, buf = buf + 1 < kRing ? buf + 1 : 0) {
             issue(t + (kRing - 1) * kBatch, buf ? buf - 1 : kRing - 1);
             copies_done<kRing - 1>();
+            In::arrive(xnow, x, D, t, end);
+            In::arrive(gnow, dy, D, t, end);
             if (t >= t0 + W - 1 && t + kBatch <= min(t1, n)) {
                 xs = dx + (size_t)(t - (W - 1)) * D;
 #pragma unroll
@@ -402,15 +419,22 @@ template <typename T, int VEC, int W> void run_step(const ConvArgs &a, cudaStrea
     conv_step_kernel<T, VEC, W><<<(unsigned)((n + kStepThreads - 1) / kStepThreads), kStepThreads, 0, s>>>(a);
 }
 
+// The channels of an access: the most, up to MOST (bf16) or 4 (fp32), that divide D and so start
+// every row's accesses on a multiple of their size.
+int access_size(int D, int most) {
+    int v = most;
+    while (D % v) v /= 2;
+    return v;
+}
 struct BwdPlan {
     int vec, CV, run, nrb;     // elements a thread, channel vectors a CTA, tokens a run, CTAs a sequence
     int ncb, rows;             // CTAs along the channels; rows of partials (one per CTA along the tokens)
 };
-// A thread of the backward takes four channels (its filter, its gradient, the window and
-// the pending outputs are 16 W floats); channels that are no multiple of four go one by one.
+// A thread of the backward takes up to four channels: its filter, its gradient, the window and the
+// pending outputs are then 16 W floats.
 BwdPlan bwd_plan(int B, int T, int D) {
     BwdPlan p;
-    p.vec = D % 4 == 0 ? 4 : 1;
+    p.vec = access_size(D, 4);
     const int ncv = D / p.vec;
     p.CV = 32;
     while (p.CV > 1 && p.CV / 2 >= ncv) p.CV /= 2;
@@ -444,13 +468,18 @@ template <typename T, int VEC, typename F> void with_taps(int W, F f) {
     else if (W == 3) f(Inst<T, VEC, 3>());
     else f(Inst<T, VEC, 4>());
 }
-// Channels that fill 16-byte accesses in every row go VECB (bf16) or 4 (fp32) at a time.
-template <int VECB, typename F> void with_inst(int dtype, int D, int W, F f) {
+template <int MOST, typename F> void with_inst(int dtype, int D, int W, F f) {
+    const int v = access_size(D, dtype == kBF16 ? MOST : 4);
     if (dtype == kBF16) {
-        if (D % VECB == 0) with_taps<__nv_bfloat16, VECB>(W, f);
+        if (v == 8) {
+            if constexpr (MOST == 8) with_taps<__nv_bfloat16, 8>(W, f);
+        }
+        else if (v == 4) with_taps<__nv_bfloat16, 4>(W, f);
+        else if (v == 2) with_taps<__nv_bfloat16, 2>(W, f);
         else with_taps<__nv_bfloat16, 1>(W, f);
     } else {
-        if (D % 4 == 0) with_taps<float, 4>(W, f);
+        if (v == 4) with_taps<float, 4>(W, f);
+        else if (v == 2) with_taps<float, 2>(W, f);
         else with_taps<float, 1>(W, f);
     }
 }

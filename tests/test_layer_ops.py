@@ -292,6 +292,7 @@ CONV = [  # B, T, D, W, dtype, silu, bias, s0, lens
     (2, 257, 1028, 4, BF16, True, True, False, False), (1, 1000, 24, 2, BF16, False, False, False, False),
     (5, 3, 12, 3, BF16, True, True, True, True), (2, 130, 513, 4, F32, True, True, True, True),
     (2, 64, 260, 3, BF16, True, True, True, False), (1, 4100, 16, 4, F32, True, True, True, False),
+    (2, 75, 130, 4, BF16, True, True, True, True), (2, 40, 50, 2, F32, True, True, True, True),
 ]
 
 
@@ -443,6 +444,8 @@ NORM = [  # M, H, d, dtype, affine, gate, center, silu
     (7, 2, 1000, F32, True, False, False, True), (6, 1, 1001, BF16, True, True, True, True), (5, 1, 2048, BF16, True, True, False, True),
     (4, 2, 4096, F32, True, True, True, True), (3, 1, 5000, BF16, True, True, True, True), (2, 1, 8192, F32, True, False, True, True),
     (2, 1, 8191, BF16, False, True, True, True), (2500, 2, 100, F32, True, True, True, True), (40, 3, 33, BF16, True, True, True, True),
+    (30, 4, 100, BF16, True, True, True, True), (11, 2, 250, F32, True, True, True, True), (3, 2, 1500, BF16, True, False, True, True),
+    (2, 1, 8190, F32, True, True, False, True), (4, 1, 3002, BF16, True, True, True, True),
 ]
 
 
