@@ -15,15 +15,20 @@ namespace qd {
 namespace {
 
 constexpr int kNormThreads = 256;
+// Threads on an SM: the backward's registers leave room for these.
+constexpr int kFwdThreads = 2048;
+__host__ __device__ constexpr int bwd_threads(int K) { return K == 1 ? 768 : 512; }
+// Threads of a CTA: one group's when it takes more than a warp.
+__host__ __device__ constexpr int cta_threads(int LPG) { return LPG > 32 ? LPG : kNormThreads; }
 
-// How a CTA's threads cover the groups: LPG threads to a group (a power of two up to 32, or
-// the whole CTA), HB groups of one token side by side, MB tokens at once.
+// How a CTA's threads cover the groups: lpg threads to a group (a power of two up to 32, or a
+// whole CTA of 128, 256 or 512), HB groups of one token side by side, MB tokens at once.
 struct NormPlan {
     int lpg, HB, MB, nhb, gm;
 };
 
-// LPG: the threads of a group (a power of two up to 32, or the whole CTA), or 0 where only the
-// plan knows (up to 32).  LPG = 16 is the instance of groups that fill their lanes (128 channels in
+// LPG: the threads of a group (16, 32, or a whole CTA's 128, 256 or 512), or 0 where only the plan
+// knows (up to 32).  LPG = 16 is the instance of groups that fill their lanes (128 channels in
 // bf16, 64 in fp32: the usual head): nothing has to be masked inside a group.
 template <int LPG, int CNT> __device__ __forceinline__ void group_totals(float (&v)[CNT], int lpg, float *sm) {
     const int n = LPG ? LPG : lpg;
@@ -47,7 +52,7 @@ template <int LPG, int CNT> __device__ __forceinline__ void group_totals(float (
         for (int i = 0; i < CNT; ++i) {
             v[i] = 0.f;
 #pragma unroll
-            for (int q = 0; q < kNormThreads / 32; ++q) v[i] += sm[q * CNT + i];
+            for (int q = 0; q < cta_threads(LPG) / 32; ++q) v[i] += sm[q * CNT + i];
         }
     }
 }
@@ -128,9 +133,9 @@ __device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K
 }
 
 template <typename T, int VEC, int K, int LPG>
-__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, NormPlan p) {
+__global__ void __launch_bounds__(cta_threads(LPG)) norm_fwd_kernel(NormArgs a, NormPlan p) {
     constexpr int HV = (VEC + 1) / 2;
-    __shared__ float sm[kNormThreads / 32];
+    __shared__ float sm[cta_threads(LPG) / 32];
     const Place<VEC, K> at(a, p);
     f32x2 w[K][HV], b[K][HV];
     at.param(a.w, a.d, 1.f, w);
@@ -195,9 +200,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a, Norm
 }
 
 template <typename T, int VEC, int K, int LPG>
-__global__ void __launch_bounds__(kNormThreads, K == 1 && LPG <= 32 ? 3 : 1) norm_bwd_kernel(NormArgs a, NormPlan p) {
+__global__ void __launch_bounds__(cta_threads(LPG), K * VEC > 8 ? 1 : bwd_threads(K) / cta_threads(LPG)) norm_bwd_kernel(NormArgs a, NormPlan p) {
     constexpr int HV = (VEC + 1) / 2;
-    __shared__ float sm[2 * kNormThreads / 32];
+    __shared__ float sm[2 * cta_threads(LPG) / 32];
     extern __shared__ float sp[];
     const Place<VEC, K> at(a, p);
     f32x2 w[K][HV], b[K][HV], dw[K][HV] = {}, db[K][HV] = {};
@@ -332,55 +337,64 @@ struct NormShape {
     int vec, K;
     NormPlan p;
 };
-// The group's accesses are shared out over the fewest lanes of a warp that take it one
-// access each (or four, on a whole warp), and over a whole CTA beyond that.  The grid holds
-// about eight CTAs per SM, which then walk the tokens.
-NormShape norm_shape(int M, int H, int d, int dtype, int ctas_per_sm) {
+// A thread holds up to 8 channels (bf16: one 16-byte access, or the 4- or 2-byte ones that odd
+// widths leave; fp32: two): fewer keep its lanes' shuffles busier than its loads, and with 32 a
+// lane needs 250 registers (1000 channels, bf16: 42 us forward, 131 us backward at 20000 groups,
+// 27 and 59 us at 8).  The group goes to the fewest lanes of a warp, or to the smallest CTA, that
+// take it so; beyond 4096 channels a thread holds 16.  The grid fills the SMs once and
+// walks the tokens.
+NormShape norm_shape(int M, int H, int d, int dtype, bool back) {
     NormShape s;
     const int wide = dtype == kBF16 ? 8 : 4;
     s.vec = d % wide == 0 ? wide : d % 2 == 0 ? 2 : 1;
-    const int nv = d / s.vec;
-    if (nv <= 32) {
-        s.p.lpg = 1;
-        while (s.p.lpg < nv) s.p.lpg *= 2;
-        s.K = 1;
-    } else if (nv <= 128) {
-        s.p.lpg = 32;
-        s.K = nv <= 64 && s.vec > 1 ? 2 : 4;
-    } else {
-        s.p.lpg = kNormThreads;
-        s.K = nv <= kNormThreads && s.vec > 1 ? 1 : nv <= 4 * kNormThreads ? 4 : s.vec == 4 ? 8 : s.vec == 2 ? 16 : 32;
-    }
-    const int slots = kNormThreads / s.p.lpg;
+    const int nv = d / s.vec, most = 8 / s.vec;        // accesses of a group; of a thread
+    s.K = 1;
+    while (s.K < most && nv > 32 * s.K) s.K *= 2;
+    s.p.lpg = s.K > 1 ? 32 : 1;
+    while (s.p.lpg < 512 && s.p.lpg * s.K < nv) s.p.lpg *= 2;
+    if (s.p.lpg == 64) s.p.lpg = 128;
+    if (s.p.lpg * s.K < nv) s.K *= 2;
+    const int nt = cta_threads(s.p.lpg), slots = nt / s.p.lpg, ctas_per_sm = s.K > most ? 1 : (back ? bwd_threads(s.K) : kFwdThreads) / nt;
     s.p.HB = H < slots ? H : slots;
     s.p.MB = slots / s.p.HB;
     s.p.nhb = (H + s.p.HB - 1) / s.p.HB;
-    const int64_t most = ((int64_t)M + s.p.MB - 1) / s.p.MB;
+    const int64_t turns = ((int64_t)M + s.p.MB - 1) / s.p.MB;
     int64_t gm = ((int64_t)ctas_per_sm * kSMs + s.p.nhb - 1) / s.p.nhb;
-    if (gm > most) gm = most;
+    if (gm > turns) gm = turns;
     s.p.gm = (int)gm;
     return s;
 }
 
 template <typename T, int VEC, int K, int LPG> void run_fwd(const NormArgs &a, const NormPlan &p, cudaStream_t s) {
-    norm_fwd_kernel<T, VEC, K, LPG><<<(unsigned)(p.gm * p.nhb), kNormThreads, 0, s>>>(a, p);
+    norm_fwd_kernel<T, VEC, K, LPG><<<(unsigned)(p.gm * p.nhb), cta_threads(LPG), 0, s>>>(a, p);
 }
 template <typename T, int VEC, int K, int LPG> void run_bwd(const NormArgs &a, const NormPlan &p, cudaStream_t s) {
     const size_t smem = (size_t)(p.MB - 1) * p.HB * p.lpg * VEC * K * sizeof(float);
-    norm_bwd_kernel<T, VEC, K, LPG><<<(unsigned)(p.gm * p.nhb), kNormThreads, smem, s>>>(a, p);
+    norm_bwd_kernel<T, VEC, K, LPG><<<(unsigned)(p.gm * p.nhb), cta_threads(LPG), smem, s>>>(a, p);
 }
 template <typename T, int VEC> void run(bool back, const NormArgs &a, const NormShape &s, cudaStream_t st) {
 #define QD_NORM_K(k, l) back ? run_bwd<T, VEC, k, l>(a, s.p, st) : run_fwd<T, VEC, k, l>(a, s.p, st)
-    const bool whole = s.p.lpg == kNormThreads;        // a group per CTA
-    if (s.K == 1 && whole) QD_NORM_K(1, kNormThreads);
-    else if (s.K == 1 && VEC > 2 && a.d == 16 * VEC) QD_NORM_K(1, 16);
-    else if (s.K == 1) QD_NORM_K(1, 0);
-    else if (s.K == 4 && whole) QD_NORM_K(4, kNormThreads);
-    else if (s.K == 4) QD_NORM_K(4, 32);
-    else if constexpr (VEC == 1) QD_NORM_K(32, kNormThreads);
-    else if (s.K == 2) QD_NORM_K(2, 32);
-    else if constexpr (VEC == 4) QD_NORM_K(8, kNormThreads);
-    else if constexpr (VEC == 2) QD_NORM_K(16, kNormThreads);
+    constexpr int MOST = 8 / VEC;
+    if (s.K > MOST) QD_NORM_K(2 * MOST, 512);
+    else if (s.p.lpg == 512) QD_NORM_K(MOST, 512);
+    else if (s.p.lpg == 256) QD_NORM_K(MOST, 256);
+    else if (s.p.lpg == 128) QD_NORM_K(MOST, 128);
+    else if (s.K == 1) {
+        if constexpr (VEC > 2) {
+            if (a.d == 16 * VEC) {
+                QD_NORM_K(1, 16);
+                return;
+            }
+        }
+        QD_NORM_K(1, 0);
+    }
+    else if constexpr (MOST > 1) {
+        if (s.K == MOST) QD_NORM_K(MOST, 32);
+        else if constexpr (MOST > 2) {
+            if (s.K == 2) QD_NORM_K(2, 32);
+            else if constexpr (MOST > 4) QD_NORM_K(4, 32);
+        }
+    }
 #undef QD_NORM_K
 }
 
@@ -399,20 +413,18 @@ cudaError_t launch(bool back, const NormArgs &a, const NormShape &s, int dtype, 
     return e;
 }
 
-constexpr int kFwdCtas = 8, kBwdCtas = 3;
-
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormArgs &a, int dtype, cudaStream_t s, int *nlaunch) {
-    return launch(false, a, norm_shape(a.M, a.H, a.d, dtype, kFwdCtas), dtype, s, nlaunch);
+    return launch(false, a, norm_shape(a.M, a.H, a.d, dtype, false), dtype, s, nlaunch);
 }
 
 size_t norm_bwd_workspace(int M, int H, int d, int dtype) {
-    return (size_t)norm_shape(M, H, d, dtype, kBwdCtas).p.gm * 2 * H * d * sizeof(float);
+    return (size_t)norm_shape(M, H, d, dtype, true).p.gm * 2 * H * d * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs &a, int dtype, cudaStream_t s, int *nlaunch) {
-    const NormShape sh = norm_shape(a.M, a.H, a.d, dtype, kBwdCtas);
+    const NormShape sh = norm_shape(a.M, a.H, a.d, dtype, true);
     if (a.M > 0) {
         const cudaError_t e = launch(true, a, sh, dtype, s, nlaunch);
         if (e != cudaSuccess) return e;
