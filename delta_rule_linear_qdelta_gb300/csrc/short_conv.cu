@@ -9,6 +9,9 @@
 // inputs in registers, so x is read once but for the W - 1 tokens before (backward: and
 // after) each run.  The tokens ahead arrive by asynchronous copies in a ring of shared memory
 // that only this thread uses: no barrier, and registers hold the filters, not the loads.
+// 8 x 2048 tokens x 2048 channels, 4 taps, bf16: forward 28.7 us (4670 GB/s, 69 % of the copy
+// bandwidth; four CTAs an SM, five spill: 30.7 us), backward 55 us with the sum of the partials
+// (3640 GB/s; loads prefetched into registers: 225 us at one CTA an SM).
 #include <type_traits>
 
 #include "layer_common.cuh"

@@ -4,7 +4,7 @@
 // Few channels over many tokens leave SMs idle, so the tokens are then cut into S segments.  A
 // first launch takes every segment but the last from a zero state (segment 0 from S0) to its
 // end E_s and its sum of u, U_s; in the second, a segment folds the ends before it,
-// h <- exp(A U_s) h + E_s, and runs as usual.  The first launch costs about 0.6 of the second.
+// h <- exp(A U_s) h + E_s, and runs as usual.  The first launch costs about 0.65 of the second.
 #include "layer_common.cuh"
 #include "ssm_scan.cuh"
 
@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmArgs a, int per_g
     }
 }
 
-// Segments: none while every SM has a CTA (256 CTAs of 8 x 2048 tokens x 2048 channels: 275 us
-// whole, 293 and 316 us in four and two segments, bf16); otherwise enough for four CTAs per SM
-// (32 CTAs of 1 x 32768 x 2048: 578 us, 633 us at three).
+// Segments: none while every SM has a CTA (256 CTAs of 8 x 2048 tokens x 2048 channels: 228 us
+// whole, 254 and 256 us in two and four segments, bf16); otherwise enough for four CTAs per SM
+// (32 CTAs of 1 x 32768 x 2048: 507 us, 545 us at three).
 Split fwd_split(int B, int T, int D, int G, int N) {
     return split_tokens(scan_ctas(B, D, G, N), T, kSMs, 4 * kSMs, 4 * kTile, kTile);
 }
