@@ -17,7 +17,7 @@ qd_status fail(qd_status s, const char *fmt, ...) {
     return qd::report_error(s, msg);
 }
 
-constexpr int64_t kMostElements = (int64_t)1 << 37;   // keeps every grid within 2^31 - 1 CTAs
+constexpr double kMostElements = 68719476736.0, kMostCtas = 2147483647.0;   // 2^36; of one launch
 
 struct Named {
     const char *name;
@@ -36,7 +36,7 @@ qd_status check_pointers(const char *fn, const Named *args, int n) {
 qd_status check_sizes(const char *fn, int B, int T, int D, qd_dtype dt) {
     if (B < 0 || T < 0 || D < 0) return fail(QD_ERR_ARG, "%s: negative size B=%d T=%d D=%d", fn, B, T, D);
     if (dt != QD_F32 && dt != QD_BF16) return fail(QD_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dt);
-    if ((double)B * (T > 1 ? T : 1) * D > (double)kMostElements) return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
+    if ((double)B * (T > 1 ? T : 1) * D > kMostElements) return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
     return QD_OK;
 }
 
@@ -49,7 +49,9 @@ qd_status check_ssm(const char *fn, int B, int T, int D, int G, int N, qd_dtype 
     if (st != QD_OK) return st;
     if (N < 1 || N > 128) return fail(QD_ERR_UNSUPPORTED, "%s: %d states per channel not in 1..128", fn, N);
     if (G < 1 || D % G) return fail(QD_ERR_ARG, "%s: D=%d is no multiple of the %d groups", fn, D, G);
-    if ((double)B * (T > 1 ? T : 1) * G * N > (double)kMostElements || (double)B * D * N > (double)kMostElements)
+    // the arrays; the scan's CTAs (of at least 8 channels of a group); the sums of dB and dC
+    if ((double)B * (T > 1 ? T : 1) * G * (N > 8 ? N : 8) > kMostElements || (double)B * D * N > kMostElements ||
+        (double)B * G * ((D / G + 7) / 8) > kMostCtas)
         return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
     return QD_OK;
 }
@@ -58,7 +60,7 @@ qd_status check_norm(const char *fn, int M, int H, int d, float eps, qd_dtype dt
     if (M < 0 || H < 0 || d < 1) return fail(QD_ERR_ARG, "%s: bad size M=%d H=%d d=%d", fn, M, H, d);
     if (dt != QD_F32 && dt != QD_BF16) return fail(QD_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dt);
     if (d > 8192) return fail(QD_ERR_UNSUPPORTED, "%s: group of %d channels (at most 8192)", fn, d);
-    if ((double)M * H * d > (double)kMostElements || (double)H * d > 2147483647.0)
+    if ((double)M * H * d > kMostElements || (double)H * d > 2147483647.0)
         return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
     if (!(eps > 0.f)) return fail(QD_ERR_ARG, "%s: eps must be positive", fn);
     return QD_OK;
@@ -135,6 +137,7 @@ qd_status short_conv_bwd(const void *x, const float *w, const float *bias, const
                           {"dy", dy, tok}, {"dS_final", dS_final, false}, {"dx", dx, tok}, {"dw", dw, D > 0},
                           {"dbias", dbias, false}, {"dS0", dS0, false}, {"workspace", workspace, false}};
     QD_CHECK_POINTERS(fn, args);
+    if (some && qd::conv_bwd_ctas(B, T, D) > kMostCtas) return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
     QD_TRY(check_workspace(fn, workspace, workspace_bytes, short_conv_bwd_workspace_bytes(B, T, D, W, dtype)));
     if (!D) return qd::end_call(0);
     int n = 0;

@@ -295,6 +295,7 @@ cudaError_t launch_conv_fwd(const ConvArgs &a, int dtype, cudaStream_t s, int *n
 cudaError_t launch_conv_step(const ConvArgs &a, int dtype, cudaStream_t s, int *nlaunch);
 cudaError_t launch_conv_bwd(const ConvBwdArgs &a, int dtype, cudaStream_t s, int *nlaunch);
 size_t conv_bwd_workspace(int B, int T, int D, int W);
+double conv_bwd_ctas(int B, int T, int D);
 cudaError_t launch_ssm_fwd(const SsmArgs &a, int dtype, cudaStream_t s, int *nlaunch);
 cudaError_t launch_ssm_step(const SsmArgs &a, int dtype, cudaStream_t s, int *nlaunch);
 cudaError_t launch_ssm_bwd(const SsmArgs &a, int dtype, cudaStream_t s, int *nlaunch);

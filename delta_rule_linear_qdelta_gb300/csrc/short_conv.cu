@@ -431,7 +431,8 @@ int access_size(int D, int most) {
 }
 struct BwdPlan {
     int vec, CV, run, nrb;     // elements a thread, channel vectors a CTA, tokens a run, CTAs a sequence
-    int ncb, rows;             // CTAs along the channels; rows of partials (one per CTA along the tokens)
+    int ncb;                   // CTAs along the channels
+    int64_t rows;              // rows of partials (one per CTA along the tokens)
 };
 // A thread of the backward takes up to four channels: its filter, its gradient, the window and the
 // pending outputs are then 16 W floats.
@@ -445,7 +446,7 @@ BwdPlan bwd_plan(int B, int T, int D) {
     p.ncb = (ncv + p.CV - 1) / p.CV;
     p.run = best_run(T, kBwdCtas * kSMs, 24, [&](int run) { return (int64_t)B * p.ncb * ((T + run * RB - 1) / (run * RB)); });
     p.nrb = T > 0 ? (T + p.run * RB - 1) / (p.run * RB) : 1;
-    p.rows = B * p.nrb;
+    p.rows = (int64_t)B * p.nrb;
     return p;
 }
 
@@ -456,7 +457,7 @@ template <typename T, int VEC, int W> cudaError_t run_bwd(const ConvBwdArgs &a, 
         const cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, VEC, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    conv_bwd_kernel<T, VEC, W><<<(unsigned)p.ncb * p.rows, kBwdThreads, smem, s>>>(a, p.CV, p.run, p.nrb, p.ncb);
+    conv_bwd_kernel<T, VEC, W><<<(unsigned)(p.ncb * p.rows), kBwdThreads, smem, s>>>(a, p.CV, p.run, p.nrb, p.ncb);
     return cudaGetLastError();
 }
 
@@ -505,6 +506,11 @@ cudaError_t launch_conv_step(const ConvArgs &a, int dtype, cudaStream_t s, int *
     return launched(nlaunch);
 }
 
+double conv_bwd_ctas(int B, int T, int D) {
+    const BwdPlan p = bwd_plan(B, T, D);
+    return (double)p.ncb * (double)p.rows;
+}
+
 size_t conv_bwd_workspace(int B, int T, int D, int W) {
     return (size_t)bwd_plan(B, T, D).rows * D * (W + 1) * sizeof(float);
 }
@@ -517,7 +523,7 @@ cudaError_t launch_conv_bwd(const ConvBwdArgs &a, int dtype, cudaStream_t s, int
         if (e != cudaSuccess) return e;
         *nlaunch += 1;
     }
-    return launch_sum_rows(a.part, p.rows, (int64_t)a.D * (a.W + 1), a.dw, (int64_t)a.D * a.W, a.dbias, a.D, nullptr, s,
+    return launch_sum_rows(a.part, (int)p.rows, (int64_t)a.D * (a.W + 1), a.dw, (int64_t)a.D * a.W, a.dbias, a.D, nullptr, s,
                            nlaunch);
 }
 

@@ -5,13 +5,16 @@ has the formulas); every tensor is contiguous and on one CUDA device.
 
 Shared arguments: activations are bfloat16 or float32, one dtype per call; parameters,
 their gradients and the scan's state are float32.  lens [B] int32 (or None): tokens from
-lens[b] on are padding, whose inputs are not used and whose outputs and gradients are 0.
+lens[b] on are padding, whose inputs are not used and whose outputs and gradients are 0.  Every
+call also takes stream= (a torch stream or a handle), on which all of it is then done.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
-from . import _check, _dtype_code, _need, _same_device, _stream, load_library
+from . import _check, _dtype_code, _need, _same_device, load_library
 
 F32, I32 = torch.float32, torch.int32
 
@@ -51,19 +54,33 @@ def _scratch(nbytes, workspace, dev):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _run(name, dev, stream, *args):
-    """Calls the entry point `name` with `dev` current and the stream as its last argument."""
+def _run(name, dev, *args):
+    """Calls the entry point `name` with `dev` current and the current stream as its last argument."""
     fn = getattr(load_library(), name)
-    st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream, dev)
     if torch._C._cuda_getDevice() == dev.index:
-        _check(fn(*args, st), name)
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, st), name)
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
 
 
-def short_conv_fwd(x, w, bias=None, S0=None, *, lens=None, silu=True, y=None, S_final=None, return_final=True,
-                   stream=None):
+def _on_stream(call):
+    """Adds the argument `stream` (a torch stream or a handle; None: the current one).  The whole call
+    is made on it, so outputs and scratch belong to it: PyTorch does not give scratch that a kernel
+    there still uses to another stream."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=next(a for a in args if a is not None).device)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on
+
+
+@_on_stream
+def short_conv_fwd(x, w, bias=None, S0=None, *, lens=None, silu=True, y=None, S_final=None, return_final=True):
     """Depthwise causal convolution over tokens with an optional SiLU.  x [B,T,D]; w [D,W]
     (W = 2, 3 or 4), bias [D] or None; S0 [B,W-1,D] in x's dtype: the inputs just before
     the call, or None (= 0).  Returns (y, S_final), S_final the last W - 1 inputs."""
@@ -75,11 +92,12 @@ def short_conv_fwd(x, w, bias=None, S0=None, *, lens=None, silu=True, y=None, S_
     y = _new(y, "y", dt, (B, T, D), dev)
     if S_final is not None or return_final:
         S_final = _new(S_final, "S_final", dt, (B, W - 1, D), dev)
-    _run("short_conv_fwd", dev, stream, *args, y.data_ptr(), _adr(S_final), B, T, D, W, int(silu), code)
+    _run("short_conv_fwd", dev, *args, y.data_ptr(), _adr(S_final), B, T, D, W, int(silu), code)
     return y, S_final
 
 
-def short_conv_step(S, x, w, bias=None, *, silu=True, y=None, stream=None):
+@_on_stream
+def short_conv_step(S, x, w, bias=None, *, silu=True, y=None):
     """One token of the convolution: x [N,D]; S [N,W-1,D] in x's dtype, the last W - 1
     inputs, updated in place.  Returns y [N,D]."""
     N, D = x.shape
@@ -88,7 +106,7 @@ def short_conv_step(S, x, w, bias=None, *, silu=True, y=None, stream=None):
             _arg(bias, "bias", F32, (D,), dev, True))
     code = _dtype_code(x)
     y = torch.empty_like(x) if y is None else _new(y, "y", dt, (N, D), dev)
-    _run("short_conv_step", dev, stream, *args, y.data_ptr(), N, D, W, int(silu), code)
+    _run("short_conv_step", dev, *args, y.data_ptr(), N, D, W, int(silu), code)
     return y
 
 
@@ -96,8 +114,8 @@ def short_conv_bwd_workspace_bytes(B, T, D, W, dtype) -> int:
     return load_library().short_conv_bwd_workspace_bytes(B, T, D, W, dtype)
 
 
-def short_conv_bwd(x, w, bias, S0, dy, dS_final=None, *, lens=None, silu=True, want_dS0=True, workspace=None,
-                   stream=None):
+@_on_stream
+def short_conv_bwd(x, w, bias, S0, dy, dS_final=None, *, lens=None, silu=True, want_dS0=True, workspace=None):
     """Backward of short_conv_fwd: gradients of sum(dy * y) + sum(dS_final * S_final).
     Returns a dict dx, dw, dbias (None without a bias), dS0 (None unless want_dS0)."""
     B, T, D = x.shape
@@ -110,7 +128,7 @@ def short_conv_bwd(x, w, bias, S0, dy, dS_final=None, *, lens=None, silu=True, w
          "dbias": None if bias is None else torch.empty_like(bias),
          "dS0": torch.empty((B, W - 1, D), dtype=dt, device=dev) if want_dS0 else None}
     ws, wsb, hold = _scratch(short_conv_bwd_workspace_bytes(B, T, D, W, code), workspace, dev)
-    _run("short_conv_bwd", dev, stream, *args, *map(_adr, g.values()), B, T, D, W, int(silu), code, ws, wsb)
+    _run("short_conv_bwd", dev, *args, *map(_adr, g.values()), B, T, D, W, int(silu), code, ws, wsb)
     return g
 
 
@@ -128,8 +146,9 @@ def ssm_workspace_bytes(B, T, D, G, N, dtype) -> int:
     return load_library().ssm_workspace_bytes(B, T, D, G, N, dtype)
 
 
+@_on_stream
 def ssm_fwd(x, delta, A, B, C, D=None, delta_bias=None, S0=None, *, lens=None, softplus=True, y=None, S_final=None,
-            return_final=True, workspace=None, stream=None):
+            return_final=True, workspace=None):
     """Selective state space scan.  x, delta [B,T,D]; A [D,N] (negative: the decay rates); B, C
     [B,T,G,N], shared by the D/G channels of a group; skip weight D [D] and delta_bias [D] or
     None; S0 [B,D,N] or None.  The step size is softplus(delta + delta_bias), or the sum itself
@@ -141,18 +160,19 @@ def ssm_fwd(x, delta, A, B, C, D=None, delta_bias=None, S0=None, *, lens=None, s
     if S_final is not None or return_final:
         S_final = _new(S_final, "S_final", F32, (nb, ch, N), dev)
     ws, wsb, hold = _scratch(ssm_workspace_bytes(nb, T, ch, G, N, code), workspace, dev)
-    _run("ssm_fwd", dev, stream, *args, y.data_ptr(), _adr(S_final), nb, T, ch, G, N, int(softplus), code, ws, wsb)
+    _run("ssm_fwd", dev, *args, y.data_ptr(), _adr(S_final), nb, T, ch, G, N, int(softplus), code, ws, wsb)
     return y, S_final
 
 
-def ssm_step(S, x, delta, A, B, C, D=None, delta_bias=None, *, softplus=True, y=None, stream=None):
+@_on_stream
+def ssm_step(S, x, delta, A, B, C, D=None, delta_bias=None, *, softplus=True, y=None):
     """One token of the scan: x, delta [N,D]; B, C [N,G,states]; S [N,D,states] float32 updated in
     place; the rest as in ssm_fwd.  Returns y [N,D]."""
     nb, _ = x.shape
     args, ch, G, N, code, dev = _ssm_inputs(x, delta, A, B, C, D, delta_bias)
     S = _arg(S, "S", F32, (nb, ch, N), dev)
     y = _new(y, "y", x.dtype, (nb, ch), dev)
-    _run("ssm_step", dev, stream, S, *args, y.data_ptr(), nb, ch, G, N, int(softplus), code)
+    _run("ssm_step", dev, S, *args, y.data_ptr(), nb, ch, G, N, int(softplus), code)
     return y
 
 
@@ -160,8 +180,9 @@ def ssm_bwd_workspace_bytes(B, T, D, G, N, dtype) -> int:
     return load_library().ssm_bwd_workspace_bytes(B, T, D, G, N, dtype)
 
 
+@_on_stream
 def ssm_bwd(x, delta, A, B, C, D, delta_bias, S0, dy, dS_final=None, *, lens=None, softplus=True, want_dS0=True,
-            workspace=None, stream=None):
+            workspace=None):
     """Backward of ssm_fwd: gradients of sum(dy * y) + sum(dS_final * S_final).  Returns a dict
     dx, ddelta, dA, dB, dC, dD and ddelta_bias (None without the parameter), dS0 (None unless
     want_dS0)."""
@@ -174,7 +195,7 @@ def ssm_bwd(x, delta, A, B, C, D, delta_bias, S0, dy, dS_final=None, *, lens=Non
          "ddelta_bias": None if delta_bias is None else torch.empty_like(delta_bias),
          "dS0": torch.empty((nb, ch, N), dtype=F32, device=dev) if want_dS0 else None}
     ws, wsb, hold = _scratch(ssm_bwd_workspace_bytes(nb, T, ch, G, N, code), workspace, dev)
-    _run("ssm_bwd", dev, stream, *args, *map(_adr, g.values()), nb, T, ch, G, N, int(softplus), code, ws, wsb)
+    _run("ssm_bwd", dev, *args, *map(_adr, g.values()), nb, T, ch, G, N, int(softplus), code, ws, wsb)
     return g
 
 
@@ -189,13 +210,14 @@ def _norm_inputs(x, w, b, z):
     return args, M, H, d, _dtype_code(x), dev
 
 
-def group_norm_fwd(x, w=None, b=None, z=None, *, eps=1e-5, center=True, silu=True, y=None, stream=None):
+@_on_stream
+def group_norm_fwd(x, w=None, b=None, z=None, *, eps=1e-5, center=True, silu=True, y=None):
     """Group norm of each token's channels: x [..., H, d], H groups of d channels; w, b [H,d] or
     None (1, 0).  center=False: the root mean square in place of the mean and variance.  With a
     gate z (x's shape) y = n SiLU(z), else y = SiLU(n); silu=False: the identity in its place."""
     args, M, H, d, code, dev = _norm_inputs(x, w, b, z)
     y = _new(y, "y", x.dtype, x.shape, dev)
-    _run("group_norm_fwd", dev, stream, *args, y.data_ptr(), M, H, d, eps, int(center), int(silu), code)
+    _run("group_norm_fwd", dev, *args, y.data_ptr(), M, H, d, eps, int(center), int(silu), code)
     return y
 
 
@@ -203,7 +225,8 @@ def group_norm_bwd_workspace_bytes(M, H, d, dtype) -> int:
     return load_library().group_norm_bwd_workspace_bytes(M, H, d, dtype)
 
 
-def group_norm_bwd(x, w, b, z, dy, *, eps=1e-5, center=True, silu=True, workspace=None, stream=None):
+@_on_stream
+def group_norm_bwd(x, w, b, z, dy, *, eps=1e-5, center=True, silu=True, workspace=None):
     """Backward of group_norm_fwd: gradients of sum(dy * y).  Returns a dict dx, dz, dw, db (None
     without the input)."""
     args, M, H, d, code, dev = _norm_inputs(x, w, b, z)
@@ -212,6 +235,6 @@ def group_norm_bwd(x, w, b, z, dy, *, eps=1e-5, center=True, silu=True, workspac
          "dw": None if w is None else torch.empty_like(w), "db": None if b is None else torch.empty_like(b)}
     need = 0 if w is None and b is None else group_norm_bwd_workspace_bytes(M, H, d, code)
     ws, wsb, hold = _scratch(need, workspace, dev)
-    _run("group_norm_bwd", dev, stream, *args, dy, *map(_adr, g.values()), M, H, d, eps, int(center), int(silu), code,
+    _run("group_norm_bwd", dev, *args, dy, *map(_adr, g.values()), M, H, d, eps, int(center), int(silu), code,
          ws, wsb)
     return g

@@ -214,6 +214,9 @@ REFUSED = [
     ("short_conv_bwd", dict(workspace=None), 5, "workspace"),
     ("ssm_fwd", dict(A=None), 1, "A is NULL"), ("ssm_fwd", dict(N=0), 2, "states"), ("ssm_fwd", dict(N=129), 2, "states"),
     ("ssm_fwd", dict(G=3), 1, "groups"), ("ssm_fwd", dict(G=0), 1, "groups"), ("ssm_fwd", dict(S0=OFF), 1, "S0"),
+    ("short_conv_bwd", dict(B=2000000000, T=1, D=33), 1, "overflow"),
+    ("ssm_fwd", dict(B=1 << 20, T=1, D=1 << 16, G=1 << 16, N=1), 1, "overflow"),
+    ("ssm_step", dict(B=1 << 20, D=1 << 14, N=128), 1, "overflow"), ("group_norm_fwd", dict(M=1 << 30, d=128), 1, "overflow"),
     ("ssm_fwd", dict(T=65536), 5, "workspace"), ("ssm_fwd", dict(dtype=2), 2, "dtype"),
     ("ssm_step", dict(Cm=None), 1, "C is NULL"), ("ssm_step", dict(D=-4), 1, "negative"),
     ("ssm_bwd", dict(dB=None), 1, "dB is NULL"), ("ssm_bwd", dict(nbytes=64), 5, "workspace"),
@@ -530,6 +533,25 @@ def test_results_do_not_change_and_other_streams_work(qd, name):
     side.synchronize()
     for a, b in zip(first, again):
         assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float())), name
+
+
+@pytest.mark.gpu
+def test_the_stream_argument(qd):
+    """A call on a given stream, as an object or a handle, allocates there and runs there: what it
+    leaves behind may be reused at once by another call on that stream."""
+    d = cu(ssm_inputs(1, 1500, 16, 16, 1, F32, 2))
+    want = qd.ssm_bwd(*(d[k] for k in SSM_IN), d["dy"], d["dS_final"])
+    y = qd.ssm_fwd(*(d[k] for k in SSM_IN))[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for _ in range(3):
+            got = qd.ssm_bwd(*(d[k] for k in SSM_IN), d["dy"], d["dS_final"], stream=stream)
+            y2 = qd.ssm_fwd(*(d[k] for k in SSM_IN), stream=stream)[0]
+        side.synchronize()
+        assert torch.equal(y, y2)
+        for k in want:
+            assert torch.equal(want[k], got[k]), k
 
 
 @pytest.mark.gpu
