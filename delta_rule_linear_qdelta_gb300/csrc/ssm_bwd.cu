@@ -46,10 +46,9 @@ BwdWs bwd_ws(int B, int T, int D, int G, int N) {
     BwdWs w;
     const size_t NP = padded_states(N), bd = (size_t)B * D;
     w.nb = channel_blocks(D, G, grad_channels(N)) / G;
-    // One segment when the CTAs fill every SM's three places; otherwise two rounds of them: one
-    // round is 3 % faster at equal lengths (4 x 4096 x 1024 channels), two are 11 % faster at ragged
-    // ones (3 x 517 x 770).
-    w.sp = split_tokens((int64_t)B * G * w.nb, T, 3 * kSMs, 6 * kSMs, 8 * kChunk, kChunk);
+    // One segment when the CTAs fill every SM's two places; otherwise two rounds of them (4 x 4096 x
+    // 1024 channels: 414 us in one round, 364 in two, 363 in three; 3 x 517 x 770, ragged: 98, 71, 77).
+    w.sp = split_tokens((int64_t)B * G * w.nb, T, 2 * kSMs, 4 * kSMs, 8 * kChunk, kChunk);
     w.nck = (T + kChunk - 1) / kChunk;
     w.rows = B * w.sp.S;
     const bool multi = w.sp.S > 1;
@@ -79,7 +78,7 @@ __host__ __device__ constexpr int part_row(int LN) { return pair_row(kGradThread
 __host__ __device__ constexpr int order_size(int NP) { return kChunk * NP + 8; }
 
 template <typename T, int LN, int VEC>
-__global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
+__global__ void __launch_bounds__(kGradThreads, 2) grads_kernel(SsmArgs a, BwdWs w, float *ws) {
     constexpr int PAIRS = kGradThreads / LN, CPB = 2 * PAIRS, NP = 4 * LN, CL = 32 / LN;
     constexpr int PARTS = sum_parts(LN), NL = LN / PARTS, PR = part_row(LN);
     using St = Staging<T, kGradThreads, kChunk, CPB, NP, 3, VEC, kStages>;
@@ -280,13 +279,25 @@ __global__ void __launch_bounds__(kGradThreads, LN <= 8 ? 3 : 2) grads_kernel(Ss
                 for (int p = 0; p < 2; ++p)
                     hh[k][c][p] = fma2(decay2(uu[c], A2[c][p]), k ? hh[k ? k - 1 : 0][c][p] : h0[c][p], mul2(ux[c], Bp[p]));
         }
+        // a token's operands are loaded before the last one's sums are stored: the loads behind a store to
+        // shared memory would wait for it
+        struct Operands {
+            float4 q;
+            float2 g;
+            ulonglong2 B, C;
+        };
+        auto operands = [&](int t) {
+            return Operands{mine[t * pair_row(PAIRS)], sg[t * PAIRS + pr], *reinterpret_cast<const ulonglong2 *>(gB + t * NP),
+                            *reinterpret_cast<const ulonglong2 *>(gC + t * NP)};
+        };
+        Operands next = operands(kChunk - 1);
 #pragma unroll
         for (int t = kChunk - 1; t >= 0; --t) {
-            const float4 q = mine[t * pair_row(PAIRS)];
-            const float2 gv = sg[t * PAIRS + pr];
-            const ulonglong2 Bv = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
-            const ulonglong2 Cv = *reinterpret_cast<const ulonglong2 *>(gC + t * NP);
-            const f32x2 Bp[2] = {Bv.x, Bv.y}, Cp[2] = {Cv.x, Cv.y};
+            const Operands at_t = next;
+            if (t > 0) next = operands(t - 1);
+            const float4 q = at_t.q;
+            const float2 gv = at_t.g;
+            const f32x2 Bp[2] = {at_t.B.x, at_t.B.y}, Cp[2] = {at_t.C.x, at_t.C.y};
             const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
             const f32x2 gg[2] = {pk(gv.x, gv.x), pk(gv.y, gv.y)};
             f32x2 vB[2], vC[2];

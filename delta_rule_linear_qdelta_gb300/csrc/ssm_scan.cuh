@@ -436,13 +436,14 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         const float4 *mine = su + half * SU + from * pair_row(PAIRS) + pair_at(pr, PAIRS);
         const float *gB = sB + half * SG + from * NP + ln * 4, *gC = gB + TILE * NP;
         float *part = sy + half * SY + (from * PARTS + ln % PARTS) * YS + c0;
+        float v[kChunk][2];                                            // parts of y, stored after the last load: a store
+                                                                       // to shared memory would hold up the loads behind it
 #pragma unroll
         for (int t = 0; t < kChunk; ++t) {
             const float4 q = mine[t * pair_row(PAIRS)];
             const ulonglong2 Bq = *reinterpret_cast<const ulonglong2 *>(gB + t * NP);
             const ulonglong2 Cq = BOTH ? *reinterpret_cast<const ulonglong2 *>(gC + t * NP) : ulonglong2{};
             const f32x2 Bv[2] = {Bq.x, Bq.y}, Cv[2] = {Cq.x, Cq.y};
-            float v[2];
             if (MODE == kEnds || SEG) U = add2(U, pk(q.x, q.y));
             const f32x2 uu[2] = {pk(q.x, q.x), pk(q.y, q.y)}, ux[2] = {pk(q.z, q.z), pk(q.w, q.w)};
 #pragma unroll
@@ -459,12 +460,15 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                         R[c][p] = fma2(P[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
                     }
                 }
-                if (OUT) v[c] = sum2(acc);
+                if (OUT) v[t][c] = sum2(acc);
             }
-            if (OUT) {
-                lane_reduce<2, NL, PARTS>(v, lane);
-                if constexpr (NL == 1) *reinterpret_cast<float2 *>(part + t * PARTS * YS) = make_float2(v[0], v[1]);
-                else if (reduced_owner<2, NL, PARTS>(lane)) part[t * PARTS * YS + reduced_first<2, NL, PARTS>(lane)] = v[0];
+            if (OUT) lane_reduce<2, NL, PARTS>(v[t], lane);
+        }
+        if constexpr (OUT) {
+#pragma unroll
+            for (int t = 0; t < kChunk; ++t) {
+                if constexpr (NL == 1) *reinterpret_cast<float2 *>(part + t * PARTS * YS) = make_float2(v[t][0], v[t][1]);
+                else if (reduced_owner<2, NL, PARTS>(lane)) part[t * PARTS * YS + reduced_first<2, NL, PARTS>(lane)] = v[t][0];
             }
         }
     };
