@@ -19,7 +19,8 @@
 // are read.  The backward's checkpoints take tiles of 8 in two halves: between two barriers a warp
 // stages the next tile and computes the one at hand, and warps drift apart in what they do.
 // (With outputs that costs, for what is done once a tile then counts twice: 227 -> 246 us at
-// 8 x 2048 x 2048 x 16 in bf16.)
+// 8 x 2048 x 2048 x 16 in bf16, when parts of y were still stored between the loads; 195 us now, with
+// the shared-memory pipe at 71 % on the SMs that hold two of the 256 CTAs, 60 % on average.)
 #pragma once
 
 #include "layer_common.cuh"
