@@ -478,6 +478,21 @@ def test_norm_of_constant_and_far_off_groups(qd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 7, 15, 50, 125])
+@pytest.mark.parametrize("B", [1, 5])
+def test_ssm_step_with_states_no_multiple_of_four(qd, N, B):
+    """States are moved one by one then; a group of sequences and the last channels are not full."""
+    d = ssm_inputs(B, 1, 77, N, 1, F32, 300 + N)
+    c = cu(d)
+    y_ref, S_ref = ref.ssm_fwd(*(d[k] for k in SSM_IN))
+    S = c["S0"].clone()
+    tok = [c[k][:, 0].contiguous() for k in ("x", "delta", "B", "C")]
+    y = qd.ssm_step(S, tok[0], tok[1], c["A"], tok[2], tok[3], c["D"], c["delta_bias"])
+    close(y, y_ref[:, 0], "y")
+    close(S, S_ref, "S")
+
+
+@pytest.mark.gpu
 def test_norm_takes_any_leading_shape(qd):
     v = norm_inputs(12, 4, 32, BF16, 3)
     c = cu(v)
