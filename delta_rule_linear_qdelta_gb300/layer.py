@@ -51,6 +51,8 @@ def _scratch(nbytes, workspace, dev):
             return None, 0, None
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _same_device(dev, workspace)
+    if not workspace.is_contiguous():                   # its bytes are not where its element count says
+        raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
