@@ -19,6 +19,11 @@ qd_status fail(qd_status s, const char *fmt, ...) {
 
 constexpr double kMostElements = 68719476736.0, kMostCtas = 2147483647.0;   // 2^36; of one launch
 
+// The most tokens of a sequence, channels or groups: kernels and plans add up to 2^16 tokens (a CTA's runs)
+// or some hundred channels or groups to them in 32 bits.
+constexpr int kMostSize = 2147483647 - 131071;
+bool too_long(int a, int b) { return a > kMostSize || b > kMostSize; }
+
 struct Named {
     const char *name;
     const void *p;
@@ -36,7 +41,8 @@ qd_status check_pointers(const char *fn, const Named *args, int n) {
 qd_status check_sizes(const char *fn, int B, int T, int D, qd_dtype dt) {
     if (B < 0 || T < 0 || D < 0) return fail(QD_ERR_ARG, "%s: negative size B=%d T=%d D=%d", fn, B, T, D);
     if (dt != QD_F32 && dt != QD_BF16) return fail(QD_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dt);
-    if ((double)B * (T > 1 ? T : 1) * D > kMostElements) return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
+    if (too_long(T, D) || (double)B * (T > 1 ? T : 1) * D > kMostElements)
+        return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
     return QD_OK;
 }
 
@@ -60,7 +66,7 @@ qd_status check_norm(const char *fn, int M, int H, int d, float eps, qd_dtype dt
     if (M < 0 || H < 0 || d < 1) return fail(QD_ERR_ARG, "%s: bad size M=%d H=%d d=%d", fn, M, H, d);
     if (dt != QD_F32 && dt != QD_BF16) return fail(QD_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dt);
     if (d > 8192) return fail(QD_ERR_UNSUPPORTED, "%s: group of %d channels (at most 8192)", fn, d);
-    if ((double)M * H * d > kMostElements || (double)H * d > 2147483647.0)
+    if (too_long(H, d) || (double)M * H * d > kMostElements || (double)H * d > 2147483647.0)
         return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
     if (!(eps > 0.f)) return fail(QD_ERR_ARG, "%s: eps must be positive", fn);
     return QD_OK;
@@ -121,7 +127,7 @@ qd_status short_conv_step(void *S, const void *x, const float *w, const float *b
 
 size_t short_conv_bwd_workspace_bytes(int B, int T, int D, int W, qd_dtype dtype) {
     (void)dtype;
-    if (B <= 0 || T < 0 || D <= 0 || W < 2 || W > 4) return 0;
+    if (B <= 0 || T < 0 || D <= 0 || W < 2 || W > 4 || too_long(T, D)) return 0;
     return qd::conv_bwd_workspace(B, T, D, W);
 }
 
@@ -147,7 +153,7 @@ qd_status short_conv_bwd(const void *x, const float *w, const float *bias, const
 
 size_t ssm_workspace_bytes(int B, int T, int D, int G, int N, qd_dtype dtype) {
     (void)dtype;
-    if (B <= 0 || T <= 0 || D <= 0 || G <= 0 || D % G || N < 1 || N > 128) return 0;
+    if (B <= 0 || T <= 0 || D <= 0 || G <= 0 || D % G || N < 1 || N > 128 || too_long(T, D)) return 0;
     return qd::ssm_fwd_workspace(B, T, D, G, N);
 }
 
@@ -194,7 +200,7 @@ qd_status ssm_step(float *S, const void *x, const void *delta, const float *A, c
 
 size_t ssm_bwd_workspace_bytes(int B, int T, int D, int G, int N, qd_dtype dtype) {
     (void)dtype;
-    if (B <= 0 || T < 0 || D <= 0 || G <= 0 || D % G || N < 1 || N > 128) return 0;
+    if (B <= 0 || T < 0 || D <= 0 || G <= 0 || D % G || N < 1 || N > 128 || too_long(T, D)) return 0;
     return qd::ssm_bwd_workspace(B, T, D, G, N);
 }
 
@@ -244,7 +250,7 @@ qd_status group_norm_fwd(const void *x, const float *w, const float *b, const vo
 }
 
 size_t group_norm_bwd_workspace_bytes(int M, int H, int d, qd_dtype dtype) {
-    if (M <= 0 || H <= 0 || d < 1 || d > 8192) return 0;
+    if (M <= 0 || H <= 0 || d < 1 || d > 8192 || too_long(H, d)) return 0;
     return qd::norm_bwd_workspace(M, H, d, dtype);
 }
 

@@ -295,7 +295,8 @@ QD_API size_t eda_workspace_bytes(int B, int T, int H, int dk, int dv, int chunk
  *   (values outside 0..T are clamped).  Their inputs are never used, whatever they hold;
  *   their outputs and token gradients are written as 0; the state is the one after
  *   lens[b] tokens.
- *   Pointers are 16-byte aligned.  Any D; B, T may be 0.  Results do not depend on the run:
+ *   Pointers are 16-byte aligned.  Any D; B, T may be 0; T, D and H up to 2^31 - 2^17, arrays up to
+ *   2^36 elements.  Results do not depend on the run:
  *   sums over tokens and channels are taken in a fixed order.
  *   No output may alias an input, but S_final may be S0 (in-place carry).
  */

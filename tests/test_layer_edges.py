@@ -36,3 +36,30 @@ def test_a_workspace_has_the_memory_that_its_size_says(layer):
             layer._scratch(1024, bad, cpu)
     assert layer._scratch(1024, base, cpu)[:2] == (base.data_ptr(), 4096)
     assert layer._scratch(1024, base.view(torch.float32), cpu)[:2] == (base.data_ptr(), 4096)
+
+
+# ------------------------------------------------------------------ sizes near 2^31
+
+MOST = 2 ** 31 - 2 ** 17
+
+
+@pytest.mark.parametrize("fn,over", [
+    ("short_conv_fwd", dict(T=MOST + 1, D=1)), ("short_conv_fwd", dict(T=1, D=MOST + 1)),
+    ("short_conv_step", dict(D=MOST + 1)), ("short_conv_bwd", dict(T=MOST + 1, D=1)),
+    ("short_conv_bwd", dict(T=1, D=MOST + 1)), ("ssm_fwd", dict(T=MOST + 1, D=1, N=1)), ("ssm_fwd", dict(T=1, D=MOST + 1, N=1)),
+    ("ssm_step", dict(D=MOST + 1, N=1)), ("ssm_bwd", dict(T=MOST + 1, D=1, N=1)),
+    ("group_norm_fwd", dict(M=1, H=MOST + 1, d=1)), ("group_norm_bwd", dict(M=1, H=MOST + 1, d=1))])
+def test_sizes_whose_index_arithmetic_would_wrap_are_refused(qd, fn, over):
+    """The kernels add up to a CTA's tokens or channels to a size in 32 bits."""
+    from test_layer_ops import _lib_call
+    assert _lib_call(qd, fn, **over) == 1
+    assert fn in qd.qd_last_error() and "overflow" in qd.qd_last_error()
+
+
+def test_workspaces_of_refused_sizes_are_none(qd):
+    for T, D in ((MOST + 1, 1), (1, MOST + 1)):
+        assert qd.short_conv_bwd_workspace_bytes(1, T, D, 4, qd.QD_F32) == 0
+        assert qd.ssm_workspace_bytes(1, T, D, 1, 1, qd.QD_F32) == 0
+        assert qd.ssm_bwd_workspace_bytes(1, T, D, 1, 1, qd.QD_F32) == 0
+    assert qd.group_norm_bwd_workspace_bytes(1, MOST + 1, 1, qd.QD_F32) == 0
+    assert qd.short_conv_bwd_workspace_bytes(1, MOST, 1, 4, qd.QD_F32) > 0
