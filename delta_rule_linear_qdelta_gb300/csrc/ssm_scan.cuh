@@ -60,7 +60,7 @@ inline Split split_tokens(int64_t ctas, int T, int64_t enough, int64_t want, int
     if (S > most) S = most;
     if (S < 2) return s;
     s.len = (int)(((T + S - 1) / S + align - 1) / align * align);
-    s.S = (T + s.len - 1) / s.len;
+    s.S = (int)(((int64_t)T + s.len - 1) / s.len);     // T + len passes 2^31
     return s;
 }
 

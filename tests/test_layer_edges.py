@@ -63,3 +63,15 @@ def test_workspaces_of_refused_sizes_are_none(qd):
         assert qd.ssm_bwd_workspace_bytes(1, T, D, 1, 1, qd.QD_F32) == 0
     assert qd.group_norm_bwd_workspace_bytes(1, MOST + 1, 1, qd.QD_F32) == 0
     assert qd.short_conv_bwd_workspace_bytes(1, MOST, 1, 4, qd.QD_F32) > 0
+
+
+def test_the_plan_of_very_long_sequences(qd):
+    """19 segments of 32 channels with 128 states each: the start and the ends of 18, and their sums of u; in the backward
+    a checkpoint per 8 tokens (states and u), ends, sums and R of all 19, dB and dC per token and group, one row of
+    parameter gradients a segment; every array rounded to 64 floats."""
+    S, D, N, T = 19, 32, 128, MOST
+    assert qd.ssm_workspace_bytes(1, T, D, D, N, qd.QD_F32) == 4 * (S * D * N + (S - 1) * D)
+    up = lambda n: (n + 63) // 64 * 64
+    chunks = T // 8
+    want = up(chunks * D * N) + up(chunks * D) + 2 * up(S * D * N) + up(S * D) + up(T * D * 2 * N) + up(S * D * (N + 2))
+    assert qd.ssm_bwd_workspace_bytes(1, T, D, D, N, qd.QD_F32) == 4 * want
