@@ -40,6 +40,12 @@ def _new(t, name, dtype, shape, dev):
     return t
 
 
+def _sizes(*sizes):
+    """Refuses what the C entry points' 32-bit sizes cannot hold: it would arrive there cut off."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"a size of {max(sizes)} does not fit in 32 bits")
+
+
 def _adr(t):
     return None if t is None else t.data_ptr()
 
@@ -88,6 +94,7 @@ def short_conv_fwd(x, w, bias=None, S0=None, *, lens=None, silu=True, y=None, S_
     the call, or None (= 0).  Returns (y, S_final), S_final the last W - 1 inputs."""
     B, T, D = x.shape
     W, dt, dev = w.shape[-1], x.dtype, x.device
+    _sizes(B, T, D, W)
     args = (_arg(x, "x", dt, (B, T, D), dev), _arg(w, "w", F32, (D, W), dev), _arg(bias, "bias", F32, (D,), dev, True),
             _arg(S0, "S0", dt, (B, W - 1, D), dev, True), _arg(lens, "lens", I32, (B,), dev, True))
     code = _dtype_code(x)
@@ -104,6 +111,7 @@ def short_conv_step(S, x, w, bias=None, *, silu=True, y=None):
     inputs, updated in place.  Returns y [N,D]."""
     N, D = x.shape
     W, dt, dev = w.shape[-1], x.dtype, x.device
+    _sizes(N, D, W)
     args = (_arg(S, "S", dt, (N, W - 1, D), dev), _arg(x, "x", dt, (N, D), dev), _arg(w, "w", F32, (D, W), dev),
             _arg(bias, "bias", F32, (D,), dev, True))
     code = _dtype_code(x)
@@ -113,6 +121,7 @@ def short_conv_step(S, x, w, bias=None, *, silu=True, y=None):
 
 
 def short_conv_bwd_workspace_bytes(B, T, D, W, dtype) -> int:
+    _sizes(B, T, D, W)
     return load_library().short_conv_bwd_workspace_bytes(B, T, D, W, dtype)
 
 
@@ -122,6 +131,7 @@ def short_conv_bwd(x, w, bias, S0, dy, dS_final=None, *, lens=None, silu=True, w
     Returns a dict dx, dw, dbias (None without a bias), dS0 (None unless want_dS0)."""
     B, T, D = x.shape
     W, dt, dev = w.shape[-1], x.dtype, x.device
+    _sizes(B, T, D, W)
     args = (_arg(x, "x", dt, (B, T, D), dev), _arg(w, "w", F32, (D, W), dev), _arg(bias, "bias", F32, (D,), dev, True),
             _arg(S0, "S0", dt, (B, W - 1, D), dev, True), _arg(lens, "lens", I32, (B,), dev, True),
             _arg(dy, "dy", dt, (B, T, D), dev), _arg(dS_final, "dS_final", dt, (B, W - 1, D), dev, True))
@@ -138,6 +148,7 @@ def _ssm_inputs(x, delta, A, B, C, D, delta_bias):
     """Checks what every form of the scan takes; tokens are x's leading dimensions."""
     tok, ch, dt, dev = tuple(x.shape[:-1]), x.shape[-1], x.dtype, x.device
     N, G = A.shape[-1], B.shape[-2]
+    _sizes(*x.shape, G, N)
     args = (_arg(x, "x", dt, (*tok, ch), dev), _arg(delta, "delta", dt, (*tok, ch), dev), _arg(A, "A", F32, (ch, N), dev),
             _arg(B, "B", dt, (*tok, G, N), dev), _arg(C, "C", dt, (*tok, G, N), dev),
             _arg(D, "D", F32, (ch,), dev, True), _arg(delta_bias, "delta_bias", F32, (ch,), dev, True))
@@ -145,6 +156,7 @@ def _ssm_inputs(x, delta, A, B, C, D, delta_bias):
 
 
 def ssm_workspace_bytes(B, T, D, G, N, dtype) -> int:
+    _sizes(B, T, D, G, N)
     return load_library().ssm_workspace_bytes(B, T, D, G, N, dtype)
 
 
@@ -179,6 +191,7 @@ def ssm_step(S, x, delta, A, B, C, D=None, delta_bias=None, *, softplus=True, y=
 
 
 def ssm_bwd_workspace_bytes(B, T, D, G, N, dtype) -> int:
+    _sizes(B, T, D, G, N)
     return load_library().ssm_bwd_workspace_bytes(B, T, D, G, N, dtype)
 
 
@@ -207,6 +220,7 @@ def _norm_inputs(x, w, b, z):
     dev, (H, d), M = x.device, x.shape[-2:], 1
     for n in x.shape[:-2]:
         M *= n
+    _sizes(M, H, d)
     args = (_arg(x, "x", x.dtype, x.shape, dev), _arg(w, "w", F32, (H, d), dev, True),
             _arg(b, "b", F32, (H, d), dev, True), _arg(z, "z", x.dtype, x.shape, dev, True))
     return args, M, H, d, _dtype_code(x), dev
@@ -224,6 +238,7 @@ def group_norm_fwd(x, w=None, b=None, z=None, *, eps=1e-5, center=True, silu=Tru
 
 
 def group_norm_bwd_workspace_bytes(M, H, d, dtype) -> int:
+    _sizes(M, H, d)
     return load_library().group_norm_bwd_workspace_bytes(M, H, d, dtype)
 
 

@@ -75,3 +75,25 @@ def test_the_plan_of_very_long_sequences(qd):
     chunks = T // 8
     want = up(chunks * D * N) + up(chunks * D) + 2 * up(S * D * N) + up(S * D) + up(T * D * 2 * N) + up(S * D * (N + 2))
     assert qd.ssm_bwd_workspace_bytes(1, T, D, D, N, qd.QD_F32) == 4 * want
+
+
+def test_sizes_beyond_32_bits_are_refused_by_the_binding(qd):
+    """The C entry points take 32-bit sizes: 2^32 rows would reach them as none."""
+    big = 2 ** 32
+    x = torch.zeros(1).expand(1, big, 1)
+    w, A, bc = torch.zeros(1, 4), torch.zeros(1, 1), torch.zeros(1).expand(1, big, 1, 1)
+    tok = torch.zeros(1).expand(big, 1)
+    calls = [lambda: qd.short_conv_fwd(x, w), lambda: qd.short_conv_bwd(x, w, None, None, x),
+             lambda: qd.short_conv_step(torch.zeros(1).expand(big, 3, 1), tok, w), lambda: qd.ssm_fwd(x, x, A, bc, bc),
+             lambda: qd.ssm_bwd(x, x, A, bc, bc, None, None, None, x),
+             lambda: qd.ssm_step(torch.zeros(1).expand(big, 1, 1), tok, tok, A, bc[0], bc[0]),
+             lambda: qd.group_norm_fwd(x.unsqueeze(-1)), lambda: qd.group_norm_bwd(x.unsqueeze(-1), None, None, None, x),
+             lambda: qd.group_norm_fwd(x.view(1, 2 ** 16, 2 ** 16, 1, 1)),
+             lambda: qd.short_conv_bwd_workspace_bytes(1, big, 1, 4, qd.QD_F32),
+             lambda: qd.ssm_workspace_bytes(1, big, 1, 1, 1, qd.QD_F32),
+             lambda: qd.ssm_bwd_workspace_bytes(1, big, 1, 1, 1, qd.QD_F32),
+             lambda: qd.group_norm_bwd_workspace_bytes(big, 1, 1, qd.QD_F32)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+            pytest.fail(f"call {i} was taken")
