@@ -81,7 +81,9 @@ def _on_stream(call):
         if stream is None:
             return call(*args, **kw)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=next(a for a in args if a is not None).device)
+            dev = next(a for a in args if a is not None).device
+            # (an ExternalStream of handle 0 would be a new stream, not the default one)
+            stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
             return call(*args, **kw)
     return on

@@ -97,3 +97,38 @@ def test_sizes_beyond_32_bits_are_refused_by_the_binding(qd):
         with pytest.raises(ValueError, match="32 bits"):
             call()
             pytest.fail(f"call {i} was taken")
+
+
+# ------------------------------------------------------------------ streams
+
+class OnGpu(torch.Tensor):
+    """A tensor that says it is on the first GPU, for what the binding decides before any CUDA call."""
+    device = property(lambda self: torch.device("cuda", 0))
+
+
+def on_gpu():
+    return torch.zeros(1).as_subclass(OnGpu)
+
+
+@pytest.mark.gpu
+def test_handle_zero_is_the_default_stream(layer):
+    x, seen = torch.zeros(1, device="cuda"), layer._on_stream(lambda t: torch.cuda.current_stream().cuda_stream)
+    assert torch.cuda.default_stream().cuda_stream == 0
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert seen(x) == side.cuda_stream
+        assert seen(x, stream=0) == 0
+        assert seen(x, stream=torch.cuda.default_stream()) == 0
+    assert seen(x, stream=side.cuda_stream) == side.cuda_stream
+
+
+def test_handle_zero_needs_no_new_stream(layer, monkeypatch):
+    import contextlib
+    used = []
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda dev: ("default", dev))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device: ("external", h, device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: used.append(s) or contextlib.nullcontext())
+    call = layer._on_stream(lambda t: None)
+    call(on_gpu(), stream=0)
+    call(on_gpu(), stream=64)
+    assert used == [("default", torch.device("cuda", 0)), ("external", 64, torch.device("cuda", 0))]
