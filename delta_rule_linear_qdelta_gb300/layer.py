@@ -78,10 +78,10 @@ def _on_stream(call):
     there still uses to another stream."""
     @functools.wraps(call)
     def on(*args, stream=None, **kw):
-        if stream is None:
+        dev = None if stream is None else next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if dev is None or dev.type != "cuda":           # (no tensor on a GPU: refused by the call)
             return call(*args, **kw)
         if not isinstance(stream, torch.cuda.Stream):
-            dev = next(a for a in args if a is not None).device
             # (an ExternalStream of handle 0 would be a new stream, not the default one)
             stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):

@@ -132,3 +132,29 @@ def test_handle_zero_needs_no_new_stream(layer, monkeypatch):
     call(on_gpu(), stream=0)
     call(on_gpu(), stream=64)
     assert used == [("default", torch.device("cuda", 0)), ("external", 64, torch.device("cuda", 0))]
+
+
+def test_a_handle_with_arguments_by_name(qd, layer, monkeypatch):
+    import contextlib
+    used = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device: (h, device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: used.append(s) or contextlib.nullcontext())
+    layer._on_stream(lambda *, x=None, eps=0.0: None)(eps=1.0, x=on_gpu(), stream=64)
+    assert used == [(64, torch.device("cuda", 0))]
+    monkeypatch.undo()
+    x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
+    with pytest.raises(ValueError, match="CUDA"):                    # the call's own refusals
+        qd.short_conv_fwd(x=x, w=w, stream=64)
+    with pytest.raises(TypeError, match="required"):
+        qd.short_conv_fwd(stream=64)
+
+
+@pytest.mark.gpu
+def test_a_handle_with_arguments_by_name_on_the_gpu(qd):
+    x, w = torch.randn(2, 9, 16, device="cuda"), torch.randn(16, 4, device="cuda")
+    want = qd.short_conv_fwd(x, w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = qd.short_conv_fwd(x=x, w=w, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
