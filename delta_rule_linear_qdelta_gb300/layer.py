@@ -84,6 +84,8 @@ def _on_stream(call):
         if not isinstance(stream, torch.cuda.Stream):
             # (an ExternalStream of handle 0 would be a new stream, not the default one)
             stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"stream of {stream.device}, expected one of {dev}, where the tensors are")
         with torch.cuda.stream(stream):
             return call(*args, **kw)
     return on

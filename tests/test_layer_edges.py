@@ -158,3 +158,21 @@ def test_a_handle_with_arguments_by_name_on_the_gpu(qd):
     got = qd.short_conv_fwd(x=x, w=w, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_a_stream_of_another_device_is_refused(layer, monkeypatch):
+    """The call would run on the tensors' device, on a stream that nobody named."""
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    import contextlib
+    ran = []
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    call = layer._on_stream(lambda t: ran.append(t))
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        call(on_gpu(), stream=Stream(1))
+    assert not ran
+    call(on_gpu(), stream=Stream(0))
+    assert len(ran) == 1
