@@ -309,15 +309,14 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) conv_bwd_kernel(ConvBwd
                     g[h] = mul2(g[h], silu_grad2(p, sigmoid2(p)));
                 }
             }
-            if (!INSIDE && tt >= n) {
+            // padding adds nothing, not even 0 times what the window still holds
+            if (INSIDE || tt < n) {
 #pragma unroll
-                for (int h = 0; h < HV; ++h) g[h] = 0;
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                    for (int h = 0; h < HV; ++h) acc[j][h] = fma2(w[j][h], g[h], acc[j][h]);
             }
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-#pragma unroll
-                for (int h = 0; h < HV; ++h) acc[j][h] = fma2(w[j][h], g[h], acc[j][h]);
-            if (INSIDE || tt < t1) {
+            if (INSIDE || tt < min(t1, n)) {
 #pragma unroll
                 for (int h = 0; h < HV; ++h) {
                     db[h] = add2(db[h], g[h]);

@@ -176,3 +176,35 @@ def test_a_stream_of_another_device_is_refused(layer, monkeypatch):
     assert not ran
     call(on_gpu(), stream=Stream(0))
     assert len(ran) == 1
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dt", [(16, F32), (33, BF16), (40, BF16)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_kept_inputs_of_a_sequence_without_tokens_give_no_weight_gradient(qd, D, dt, bad):
+    """No token of it meets them, whatever they hold.  Likewise the last inputs of a sequence and its padding."""
+    g = torch.Generator().manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=g)
+    x, dy, w, bias, S0 = r(3, 9, D).to(dt), r(3, 9, D).to(dt), r(D, 4), r(D), r(3, 3, D).to(dt)
+    lens = torch.tensor([9, 0, 4], dtype=torch.int32)
+    S0[1] = bad
+    args = (x, w, bias, S0, dy, None)
+    S0_fine = S0.clone()
+    S0_fine[1] = 0.0                                     # the definition, where those rows are used by nothing
+    want = ref.conv_bwd(x, w, bias, S0_fine, dy, None, lens)
+    got = qd.short_conv_bwd(*(t if t is None else t.cuda() for t in args), lens=lens.cuda())
+    for k in ("dw", "dbias", "dx", "dS0"):
+        e = (got[k].cpu().double() - want[k]).abs()
+        # fp32: a sum of 13 terms, 2^-24 and the hardware exponential's 2^-22 each; bf16: half an ulp more
+        assert (e <= 1e-5 * want[k].abs().max() + (2.0 ** -8 * want[k].abs() if got[k].dtype is BF16 else 0)).all(), k
+
+
+@pytest.mark.gpu
+def test_an_infinite_last_input_meets_no_padding(qd):
+    """Without an activation dw is dy x: infinite where the token is, and in no other tap."""
+    x, dy, w = torch.ones(1, 8, 8, device="cuda"), torch.ones(1, 8, 8, device="cuda"), torch.ones(8, 4, device="cuda")
+    x[0, 4] = float("inf")
+    g = qd.short_conv_bwd(x, w, None, None, dy, lens=torch.tensor([5], dtype=torch.int32, device="cuda"), silu=False)
+    assert torch.equal(g["dw"], torch.tensor([2.0, 3.0, 4.0, float("inf")], device="cuda").expand(8, 4))
