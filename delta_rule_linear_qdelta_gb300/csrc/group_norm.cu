@@ -124,9 +124,10 @@ __device__ __forceinline__ float normalise(f32x2 (&v)[K][HV], const bool (&on)[K
         for (int i = 0; i < HV; ++i) q = fma2(v[k][i], v[k][i], q);
     float tot[1] = {sum2(q)};
     group_totals<LPG>(tot, lpg, sm);
-    // the hardware's reciprocal root (2 ulp) and one Newton step
+    // the hardware's reciprocal root (2 ulp) and one Newton step; an infinite sum of squares leaves 0, of which
+    // the step would make a NaN
     const float var = fmaf(tot[0], inv_d, a.eps), r0 = rsqrtf(var);
-    const float rstd = r0 * fmaf(-0.5f * var * r0, r0, 1.5f);
+    const float rstd = r0 == 0.f ? 0.f : r0 * fmaf(-0.5f * var * r0, r0, 1.5f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll

@@ -378,7 +378,8 @@ QD_API size_t ssm_bwd_workspace_bytes(int B, int T, int D, int G, int N, qd_dtyp
  *     xh = (x - mean) / sqrt(var + eps)       center = 0: x / sqrt(mean(x^2) + eps)
  *     n = xh w + b                            w, b [H][d] fp32 (NULL: 1, 0)
  *     y = act(n), or n act(z) with a gate z   act: SiLU when silu, else the identity
- * eps must be positive.
+ * eps must be positive.  Statistics are fp32: where a group's sum of squares passes that range (values
+ * from about 1e18 on) 1 / sqrt is 0, and so is xh.
  */
 QD_API qd_status group_norm_fwd(const void *x, const float *w, const float *b, const void *z, void *y, int M, int H,
                                 int d, float eps, int center, int silu, qd_dtype dtype, cudaStream_t stream);

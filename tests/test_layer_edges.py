@@ -208,3 +208,29 @@ def test_an_infinite_last_input_meets_no_padding(qd):
     x[0, 4] = float("inf")
     g = qd.short_conv_bwd(x, w, None, None, dy, lens=torch.tensor([5], dtype=torch.int32, device="cuda"), silu=False)
     assert torch.equal(g["dw"], torch.tensor([2.0, 3.0, 4.0, float("inf")], device="cuda").expand(8, 4))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,dt", [(128, BF16), (64, F32), (20, F32), (1000, BF16), (4096, F32), (33, BF16), (1, F32)])
+@pytest.mark.parametrize("center", [True, False])
+def test_a_group_whose_squares_overflow_is_normalised_to_nothing(qd, d, dt, center):
+    """Its reciprocal root is 0 (1 / sqrt(inf)), so y = act(b), and nothing flows to x and w; other groups are as ever."""
+    g = torch.Generator().manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=g)
+    x, w, b, dy = r(5, 2, d).to(dt), 1 + 0.1 * r(2, d), r(2, d), r(5, 2, d).to(dt)
+    sign = torch.where(torch.arange(d) % 2 == 0, 1.0, -1.0)
+    big = (3e19 * sign).to(dt)                           # its square is above the largest number of 32 bits, its sum is not
+    x[1, 0] = big
+    c = [t.cuda() for t in (x, w, b)]
+    y = qd.group_norm_fwd(*c, center=center, silu=False)
+    grads = qd.group_norm_bwd(*c, None, dy.cuda(), center=center, silu=False)
+    if d == 1 and center:
+        return                                           # one channel: nothing is left of it after centring
+    assert torch.equal(y[1, 0], c[2][0].to(dt)) and (grads["dx"][1, 0] == 0).all()
+    for t in (y, *(grads[k] for k in ("dx", "dw", "db"))):
+        assert torch.isfinite(t).all()
+    x[1, 0] = 0                                          # the same xh = 0 for that group
+    c = [t.cuda() for t in (x, w, b)]
+    y0 = qd.group_norm_fwd(*c, center=center, silu=False)
+    g0 = qd.group_norm_bwd(*c, None, dy.cuda(), center=center, silu=False)
+    assert torch.equal(y, y0) and torch.equal(grads["dw"], g0["dw"]) and torch.equal(grads["db"], g0["db"])
