@@ -111,6 +111,18 @@ __device__ __forceinline__ f32x2 exp2_2(f32x2 x) {
 constexpr float kDecayShift = 1e-8f;
 __device__ __forceinline__ f32x2 decay2(f32x2 u, f32x2 A2) { return exp2_2(fma2(u, A2, pk(kDecayShift, kDecayShift))); }
 __device__ __forceinline__ float decay(float u, float A2) { return exp2_fast(fmaf(u, A2, kDecayShift)); }
+// exp(U A) v + e of two states, U a sum of step sizes.  CAREFUL: U A may be large and positive; exp(U A) can
+// then overflow where the product does not, v being small or exactly 0, so it is taken in two halves,
+// kept finite, one before v and one after.
+template <bool CAREFUL> __device__ __forceinline__ f32x2 carry2(f32x2 U, f32x2 A2, f32x2 v, f32x2 e) {
+    if constexpr (!CAREFUL) return fma2(decay2(U, A2), v, e);
+    float a, b;
+    unpk(fma2(mul2(U, pk(0.5f, 0.5f)), A2, pk(kDecayShift, kDecayShift)), a, b);
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(127.f));             // 2^127 twice times the smallest normal number overflows
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(127.f));
+    const f32x2 half = pk(exp2_fast(a), exp2_fast(b));
+    return fma2(half, mul2(half, v), e);
+}
 __device__ __forceinline__ float sum2(f32x2 v) {
     float a, b;
     unpk(v, a, b);

@@ -147,22 +147,31 @@ __global__ void __launch_bounds__(kGradThreads, 2) grads_kernel(SsmArgs a, BwdWs
             A2[c][p] = mul2(A2[c][p], pk(kLog2e, kLog2e));
             dA[c][p] = hin[c][p] = 0;
         }
-        if (S > 1 && c0 + c < cb.count) {
-            for (int s = S - 1; s > seg; --s) {
-                const float U = ws[w.U + s * all + bd + c];
-                f32x2 r[2];
-                fetch(w.R, s * all + bd, c, r);
+    }
+    const bool up = S > 1 && (!a.softplus || rates_grow(A2));
+    if (S > 1) {
+        auto fold = [&](auto careful) {
 #pragma unroll
-                for (int p = 0; p < 2; ++p) dh[c][p] = fma2(decay2(pk(U, U), A2[c][p]), dh[c][p], r[p]);
-            }
-            for (int s = 0; s < seg; ++s) {
-                const float U = ws[w.U + s * all + bd + c];
-                f32x2 e[2];
-                fetch(w.E, s * all + bd, c, e);
+            for (int c = 0; c < 2; ++c) {
+                if (c0 + c >= cb.count) continue;
+                for (int s = S - 1; s > seg; --s) {
+                    const float U = ws[w.U + s * all + bd + c];
+                    f32x2 r[2];
+                    fetch(w.R, s * all + bd, c, r);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) hin[c][p] = fma2(decay2(pk(U, U), A2[c][p]), hin[c][p], e[p]);
+                    for (int p = 0; p < 2; ++p) dh[c][p] = carry2<careful.value>(pk(U, U), A2[c][p], dh[c][p], r[p]);
+                }
+                for (int s = 0; s < seg; ++s) {
+                    const float U = ws[w.U + s * all + bd + c];
+                    f32x2 e[2];
+                    fetch(w.E, s * all + bd, c, e);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) hin[c][p] = carry2<careful.value>(pk(U, U), A2[c][p], hin[c][p], e[p]);
+                }
             }
-        }
+        };
+        if (up) fold(std::true_type{});
+        else fold(std::false_type{});
     }
     float bias[VEC], skip[VEC], dDs[VEC], dbs[VEC];                    // of the channels this thread writes
     St::param(a.delta_bias, cb, bias);
@@ -266,7 +275,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) grads_kernel(SsmArgs a, BwdWs
             if (seg > 0) {
                 const float U = on ? ck_u[c] : 0.f;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) h0[c][p] = fma2(decay2(pk(U, U), A2[c][p]), hin[c][p], h0[c][p]);
+                for (int p = 0; p < 2; ++p)
+                    h0[c][p] = up ? carry2<true>(pk(U, U), A2[c][p], hin[c][p], h0[c][p])
+                                  : carry2<false>(pk(U, U), A2[c][p], hin[c][p], h0[c][p]);
             }
         }
         if (chunk > 0) checkpoint();

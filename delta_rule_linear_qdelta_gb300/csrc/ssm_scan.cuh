@@ -23,6 +23,8 @@
 // the shared-memory pipe at 71 % on the SMs that hold two of the 256 CTAs, 60 % on average.)
 #pragma once
 
+#include <type_traits>
+
 #include "layer_common.cuh"
 
 namespace qd {
@@ -68,6 +70,20 @@ inline Split split_tokens(int64_t ctas, int T, int64_t enough, int64_t want, int
 template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
     return bytes <= 48 * 1024 ? cudaSuccess
                               : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// Whether a lane of the warp holds a rate A above 0: its states grow, by more than fp32 holds over many tokens.
+__device__ __forceinline__ bool rates_grow(const f32x2 (&A2)[2][2]) {
+    bool up = false;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float lo, hi;
+            unpk(A2[c][p], lo, hi);
+            up = up || lo > 0.f || hi > 0.f;
+        }
+    return __any_sync(0xffffffffu, up);
 }
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int T) { return lens ? min(max(lens[b], 0), T) : T; }
@@ -322,19 +338,24 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         put_state(w.start, bd, 0, h[0]);
         put_state(w.start, bd, 1, h[1]);
     }
+    const bool up = (SEG || (OUT && sp.S > 1)) && rates_grow(A2);
     if (OUT && sp.S > 1) {                                             // fold the segments before this one
+        auto fold = [&](auto careful) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (c0 + c >= cb.count) continue;
-            for (int s = seg > 0 ? 0 : -1; s < max(seg, 0); ++s) {
-                const float *src = s < 0 ? w.start : w.E + s * all * NP;
-                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(src + (bd + c) * NP + ln * 4);
-                const float U = s < 0 ? 0.f : w.U[s * all + bd + c];
-                const f32x2 UU = pk(U, U);
-                h[c][0] = fma2(decay2(UU, A2[c][0]), h[c][0], e.x);
-                h[c][1] = fma2(decay2(UU, A2[c][1]), h[c][1], e.y);
+            for (int c = 0; c < 2; ++c) {
+                if (c0 + c >= cb.count) continue;
+                for (int s = seg > 0 ? 0 : -1; s < max(seg, 0); ++s) {
+                    const float *src = s < 0 ? w.start : w.E + s * all * NP;
+                    const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(src + (bd + c) * NP + ln * 4);
+                    const float U = s < 0 ? 0.f : w.U[s * all + bd + c];
+                    const f32x2 UU = pk(U, U);
+                    h[c][0] = carry2<careful.value>(UU, A2[c][0], h[c][0], e.x);
+                    h[c][1] = carry2<careful.value>(UU, A2[c][1], h[c][1], e.y);
+                }
             }
-        }
+        };
+        if (up || !a.softplus) fold(std::true_type{});
+        else fold(std::false_type{});
     }
 
     float bias[VEC], skip[VEC];
@@ -347,6 +368,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
     typename St::Cursor at = cursor();
     T *y = OUT ? (T *)a.y + ((size_t)b * a.T + t_begin + St::tok(0)) * D + cb.first + St::chan() : nullptr;
     f32x2 U = 0;                                                       // of the two channels
+    bool back = false;                                                 // SEG: a step size below 0 has been staged
 
     auto issue = [&](int t0, int slot) { St::issue(at, raw, slot, a, cb, t0, t0 < t_end, n, BOTH, 1); };
     // the tile at t0, arrived in `slot`, to half `half` of the staging arrays
@@ -360,6 +382,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
             St::get(raw, slot, 0, i, a, cb, b, t0, n, a.x, x);
             St::get(raw, slot, 1, i, a, cb, b, t0, n, a.delta, u);
             step_sizes<VEC>(u, bias, a.softplus);
+            if (SEG && !a.softplus) {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) back = back || u[k] < 0.f;
+            }
             if (!full && !(t0 + t < n && c < cb.count)) {              // of the padding nothing counts
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) u[k] = 0.f;
@@ -421,8 +447,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
         y += (size_t)TILE * D;
     };
 
-    // the kChunk tokens from `from` on of the staged tile, the first of them token tc
-    auto compute = [&](int tc, int from, int half) {
+    // the kChunk tokens from `from` on of the staged tile, the first of them token tc.  GROWS (SEG, from the
+    // first tile on that has what may grow): R takes the products P from the sums of u.
+    auto compute = [&](auto growing, int tc, int from, int half) {
+        constexpr bool GROWS = growing.value;
         if (CHK) {                                                     // tc is a checkpoint of the segment
             const size_t row = (size_t)(tc / kChunk) * all + bd;
             put_state(w.chk, row, 0, h[0]);
@@ -456,7 +484,11 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                     const f32x2 av = decay2(uu[c], A2[c][p]);
                     h[c][p] = fma2(av, h[c][p], mul2(ux[c], Bv[p]));
                     if (OUT) acc = p ? fma2(Cv[p], h[c][p], acc) : mul2(Cv[p], h[c][p]);
-                    if (SEG) {
+                    if (SEG && GROWS) {
+                        float u0, u1;
+                        unpk(U, u0, u1);
+                        R[c][p] = carry2<true>(c ? pk(u1, u1) : pk(u0, u0), A2[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
+                    } else if (SEG) {
                         P[c][p] = mul2(P[c][p], av);
                         R[c][p] = fma2(P[c][p], mul2(pk(g, g), Cv[p]), R[c][p]);
                     }
@@ -485,16 +517,21 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
             stage(t0, slot, 0);
             __syncthreads();
 #pragma unroll 1
-            for (int from = 0; from < TILE; from += kChunk) compute(t0 + from, from, 0);
+            for (int from = 0; from < TILE; from += kChunk) compute(std::false_type{}, t0 + from, from, 0);
             __syncthreads();
             if (OUT) finish(t0, slot, 0);
         }
     } else {
+        bool grows = up;                                               // from here on, for all of the CTA
+        auto staged = [&] {
+            if (SEG && !a.softplus) grows |= __syncthreads_or(back) != 0;
+            else __syncthreads();
+        };
         if (t_begin < t_end) {
             if constexpr (St::ASYNC) copies_done<AHEAD - 1>();
             stage(t_begin, 0, 0);
         }
-        __syncthreads();
+        staged();
         int half = 0;
         for (int t0 = t_begin; t0 < t_end; t0 += TILE, slot = later(slot, 1), half ^= 1) {
             issue(t0 + AHEAD * TILE, later(slot, AHEAD));
@@ -502,8 +539,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(SsmArgs a, Split 
                 if constexpr (St::ASYNC) copies_done<AHEAD - 1>();
                 stage(t0 + TILE, later(slot, 1), half ^ 1);
             }
-            compute(t0, 0, half);
-            __syncthreads();
+            if constexpr (SEG) {
+                if (grows) compute(std::true_type{}, t0, 0, half);
+                else compute(std::false_type{}, t0, 0, half);
+            } else {
+                compute(std::false_type{}, t0, 0, half);
+            }
+            staged();
         }
     }
     if constexpr (OUT) {                                               // whole tiles of padding

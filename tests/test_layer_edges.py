@@ -234,3 +234,85 @@ def test_a_group_whose_squares_overflow_is_normalised_to_nothing(qd, d, dt, cent
     y0 = qd.group_norm_fwd(*c, center=center, silu=False)
     g0 = qd.group_norm_bwd(*c, None, dy.cuda(), center=center, silu=False)
     assert torch.equal(y, y0) and torch.equal(grads["dw"], g0["dw"]) and torch.equal(grads["db"], g0["db"])
+
+
+# ------------------------------------------------------------------ states that grow
+
+GROW = [(16, 16), (7, 5), (16, 64)]                      # D, N: one CTA along the channels, so 1500 tokens are cut into segments
+
+
+def growing(D, N, seed):
+    """A > 0 and step sizes as they come; everything else 0."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)
+    z = torch.zeros(1, 1500, D)
+    return g, {"x": z.clone(), "delta": z.clone(), "A": 6 + 0.1 * r(D, N), "B": r(1, 1500, 1, N), "C": r(1, 1500, 1, N),
+               "D": None, "delta_bias": None, "S0": None, "dy": z.clone(), "dS_final": None}
+
+
+SSM_IN = ("x", "delta", "A", "B", "C", "D", "delta_bias", "S0")
+
+
+def scan_both(qd, d, tol, softplus=False):
+    assert qd.ssm_workspace_bytes(1, 1500, d["x"].shape[-1], 1, d["A"].shape[-1], qd.QD_F32) > 0
+    c = {k: None if v is None else v.cuda() for k, v in d.items()}
+    y, S = qd.ssm_fwd(*(c[k] for k in SSM_IN), softplus=softplus)
+    g = qd.ssm_bwd(*(c[k] for k in SSM_IN), c["dy"], c["dS_final"], softplus=softplus)
+    y_ref, S_ref = ref.ssm_fwd(*(d[k] for k in SSM_IN), softplus=softplus)
+    want = {"y": y_ref, "S_final": S_ref, **ref.ssm_bwd(*(d[k] for k in SSM_IN), d["dy"], d["dS_final"], softplus=softplus)}
+    for k, v in {"y": y, "S_final": S, **g}.items():
+        if want[k] is None:
+            assert v is None, k
+            continue
+        assert torch.isfinite(v).all(), k
+        err = (v.cpu().double() - want[k]).norm()
+        assert err <= tol * want[k].norm(), (k, float(err), float(want[k].norm()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,N", GROW)
+@pytest.mark.parametrize("how", ["rates", "rates and softplus", "steps back"])
+def test_a_state_of_zero_stays_zero_while_decays_overflow(qd, D, N, how):
+    """Between the tokens that send gradients and those that have inputs, exp(A u) would multiply up to e^1900, by
+    positive rates or by negative step sizes."""
+    g, d = growing(D, N, 20)
+    softplus, u = how == "rates and softplus", torch.full((1500,), 0.01)
+    u[100:1400] = 0.25
+    if how == "steps back":
+        u[100:1400] *= -1
+        d["A"] *= -1
+    d["delta"][:] = (torch.log(torch.expm1(u.double())).float() if softplus else u)[None, :, None]
+    d["x"][:, 1400:] = torch.randn(1, 100, D, generator=g)
+    d["dy"][:, :100] = torch.randn(1, 100, D, generator=g)
+    # fp32 tolerance of the scan: the tokens with inputs or gradients make 100 steps of at most e^0.07
+    scan_both(qd, d, 1e-5, softplus)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,N", GROW)
+@pytest.mark.parametrize("way", [1, -1])
+def test_a_tiny_state_grows_over_a_segment_by_more_than_fp32_holds(qd, D, N, way):
+    """1e-30 e^96 is an ordinary number.  Tolerance: the exponent, 139 as a power of two, has a relative error of 2^-24 from
+    A log2(e) and, taken at once in two halves or in 64 steps, 8e-6 from its roundings: 1.2e-5 in all, and the
+    products of a state and a gradient have it twice and the sums' 1e-5."""
+    g, d = growing(D, N, 21)
+    d["delta"][:, 80:144] = 0.25 * way
+    d["A"] *= way
+    d["S0"], d["dS_final"] = (1e-30 * torch.randn(1, D, N, generator=g) for _ in range(2))
+    scan_both(qd, d, 5e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_step_size_that_is_no_number_is_not_hidden(qd, bad):
+    g, d = growing(16, 16, 22)
+    d["delta"][:, :] = 0.01
+    d["delta"][0, 300, 3] = bad
+    d["S0"] = torch.ones(1, 16, 16)
+    c = {k: None if v is None else v.cuda() for k, v in d.items()}
+    y, S = qd.ssm_fwd(*(c[k] for k in SSM_IN), softplus=False)
+    assert not torch.isfinite(S[0, 3]).any() and not torch.isfinite(y[0, 300:, 3]).any()
+    # the other channels are finite where their definition is within fp32 (S0 e^90 is not everywhere)
+    fine = ref.ssm_fwd(*(d[k] for k in SSM_IN), softplus=False)[1][0].abs() <= torch.finfo(F32).max
+    other = torch.arange(16) != 3
+    assert torch.equal(torch.isfinite(S[0].cpu())[other], fine[other]) and torch.isfinite(y[0, :300]).all()
