@@ -316,3 +316,25 @@ def test_a_step_size_that_is_no_number_is_not_hidden(qd, bad):
     fine = ref.ssm_fwd(*(d[k] for k in SSM_IN), softplus=False)[1][0].abs() <= torch.finfo(F32).max
     other = torch.arange(16) != 3
     assert torch.equal(torch.isfinite(S[0].cpu())[other], fine[other]) and torch.isfinite(y[0, :300]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,N,dt,lens", [(16, 16, F32, None), (21, 5, F32, 30011), (24, 16, BF16, None)])
+def test_hundreds_of_segments(qd, D, N, dt, lens):
+    """Few channels over very many tokens, within the tolerances of the other scan tests: fp32 relative L2 1e-5, bf16
+    half an ulp and 1e-5 of the largest."""
+    from test_layer_ops import close, close_all, ssm_inputs
+    T = 32768
+    d = ssm_inputs(1, T, D, N, 1, dt, 500 + D)
+    assert qd.ssm_workspace_bytes(1, T, D, 1, N, qd.QD_F32) >= 4 * 400 * D * N
+    if lens:
+        d["lens"] = torch.tensor([lens], dtype=torch.int32)
+        for k in ("x", "delta", "B", "C", "dy"):
+            d[k][:, lens:] = float("nan")
+    c = {k: None if v is None else v.cuda() for k, v in d.items()}
+    y, S = qd.ssm_fwd(*(c[k] for k in SSM_IN), lens=c["lens"])
+    y_ref, S_ref = ref.ssm_fwd(*(d[k] for k in SSM_IN), d["lens"])
+    close(y, y_ref, "y")
+    close(S, S_ref, "S_final")
+    g = qd.ssm_bwd(*(c[k] for k in SSM_IN), c["dy"], c["dS_final"], lens=c["lens"])
+    close_all(g, ref.ssm_bwd(*(d[k] for k in SSM_IN), d["dy"], d["dS_final"], d["lens"]))
