@@ -10,7 +10,9 @@
 // from it, so no precision is lost where the mean is large.  A thread keeps its channels
 // from token to token, so weights are read once per thread and dw, db add up in registers.
 // 16384 tokens x 16 groups of 128, gated, bf16: forward 37 us (5410 GB/s, 80 % of the copy
-// bandwidth), backward 70 us with the sum of the partials (4790 GB/s).
+// bandwidth), backward 70 us with the sum of the partials (4790 GB/s; at its 80 registers, for three
+// CTAs an SM, it spills 36 bytes).  The backward of single accesses (odd widths above 128) spills 430 bytes
+// and more: half of each pair that it holds is empty.
 #include "layer_common.cuh"
 
 namespace qd {

@@ -18,10 +18,12 @@
 //  3. the sums over CTAs: dB, dC over the channel blocks, and dA, dD, d bias over sequences
 //     and segments; in a fixed order, so results do not change from run to run.
 // Bound by the shared-memory pipe and instruction issue: two exponentials and about 20 operations
-// per (token, channel, state) in launch 2, one and 4 in launch 1.  4 x 4096 tokens x 1024 channels x
-// 16 states, bf16: 364 us, of which launch 1 takes 100, launch 2 247 and the sums 18.  Launch 2 keeps 8
-// tokens' states in 218 registers, so 8 warps share an SM.  (Two halves of what it stages, with one
-// barrier a chunk as in launch 1, cost it 371 us in all: the code that is then there twice is slower.)
+// per (token, channel, state) in launch 2, one and 4 in launch 1, or one and 7 where it works on
+// segments (R and its products).  4 x 4096 tokens x 1024 channels x 16 states, bf16: 360 us, of which
+// launch 1 (segments) takes 100, launch 2 243 and the sums 17.  Launch 2 keeps 8 tokens' states in 216
+// registers, so 8 warps share an SM.  (Two halves of what it stages, with one barrier a chunk as in
+// launch 1, took 371 us in all against 364: the code that is then there twice is slower.)
+// States that may grow: carry2 joins segments, see there.
 #include "layer_common.cuh"
 #include "ssm_scan.cuh"
 

@@ -51,7 +51,9 @@ struct ChannelBlock {
 };
 
 // Tokens cut into S segments of `len` (a multiple of `align`, the tile): one when `ctas` CTAs
-// already number `enough`, else about `want` CTAs in all, of at least `least` tokens.
+// already number `enough`, else about `want` CTAs in all, of at least `least` tokens.  What a segment
+// spends on joining those before it is not counted: at 512 segments (1 x 32768 tokens x 16 channels x 16 states,
+// bf16) the forward takes 84 us and the backward 209, as long as with 128 channels and 293 segments (84, 199).
 struct Split {
     int S, len;
 };
@@ -146,7 +148,8 @@ template <typename T, int THREADS, int TILE, int CPB, int NP, int NA, int V, int
     // Whether the whole tile at t0 is real: no padding, no channels beyond the block's.
     __device__ __forceinline__ static bool full(const ChannelBlock &cb, int t0, int n) { return t0 + TILE <= n && cb.count == CPB; }
 
-    // A thread's place in the arrays, moved from tile to tile: addresses are worked out once.
+    // A thread's place in the arrays, moved from tile to tile: addresses are worked out once.  (g is indexed
+    // with B or C as the thread has it, so the compiler keeps the cursor in local memory: 56 or 64 bytes.)
     struct Cursor {
         const T *p[NA], *g[2], *own;                                   // tokens; the tile's B and C; this thread's if it has one access
         size_t rows;                                                   // from one token access of a tile to the next

@@ -6,7 +6,8 @@ has the formulas); every tensor is contiguous and on one CUDA device.
 Shared arguments: activations are bfloat16 or float32, one dtype per call; parameters,
 their gradients and the scan's state are float32.  lens [B] int32 (or None): tokens from
 lens[b] on are padding, whose inputs are not used and whose outputs and gradients are 0.  Every
-call also takes stream= (a torch stream or a handle), on which all of it is then done.
+call also takes stream= (a torch stream of the tensors' device, or a handle, 0 being the default
+stream), on which all of it is then done.  A workspace is any contiguous tensor of enough bytes.
 """
 from __future__ import annotations
 

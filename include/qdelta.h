@@ -362,7 +362,7 @@ QD_API qd_status ssm_step(float *S, const void *x, const void *delta, const floa
  * Outputs, each overwritten: dx, ddelta [B][T][D] and dB, dC [B][T][G][N] in the call's dtype
  * (ddelta: of the raw delta), dA [D][N] fp32 (required); dDskip [D] and ddelta_bias [D] fp32
  * when non-NULL and the parameter is; dS0 [B][D][N] fp32 when non-NULL (also when S0 is NULL).
- * workspace: at least ssm_bwd_workspace_bytes(...) bytes (the state entering every 16 tokens,
+ * workspace: at least ssm_bwd_workspace_bytes(...) bytes (the state entering every 8 tokens,
  * and partial sums).
  */
 QD_API qd_status ssm_bwd(const void *x, const void *delta, const float *A, const void *Bm, const void *Cm,
