@@ -44,15 +44,15 @@ def _decay_arg(g, dt, tok, H, dev):
     """Address of the log decays, and whether there is one for each token."""
     if g is None:
         return None, 0
-    if g.dim() == 1 and len(tok) >= 1:
+    if g.dim() == 1:
         return _arg(g, "g", F32, (H,), dev), 0
     return _arg(g, "g", dt, (*tok, H), dev), 1
 
 
-def _lin_inputs(q, k, v, g):
-    """Checks what every form of linear attention takes; tokens are q's leading dimensions."""
-    if q.dim() < 3 or v.dim() != q.dim():
-        raise ValueError(f"q, v have shapes {tuple(q.shape)}, {tuple(v.shape)}, expected [..., H, d]")
+def _lin_inputs(q, k, v, g, lead):
+    """Checks what every form of linear attention takes; tokens are q's leading dimensions, named in `lead`."""
+    if q.dim() != len(lead) + 2 or v.dim() != q.dim():
+        raise ValueError(f"q, v have shapes {tuple(q.shape)}, {tuple(v.shape)}, expected [{', '.join(lead)}, H, d]")
     tok, (H, dk), dv, dt, dev = tuple(q.shape[:-2]), q.shape[-2:], v.shape[-1], q.dtype, q.device
     _sizes(*q.shape, dv)
     gp, per_token = _decay_arg(g, dt, tok, H, dev)
@@ -71,8 +71,8 @@ def lin_attn_fwd(q, k, v, g=None, S0=None, *, lens=None, o=None, S_final=None, r
     """Linear attention: S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = S_t q_t.  q, k [B,T,H,dk]; v [B,T,H,dv];
     log decays g [B,T,H] in q's dtype (one for each token and head), [H] float32 (one for each head) or None
     (no decay), at most 0, -inf dropping the state; S0 [B,H,dv,dk] or None.  Returns (o, S_final)."""
+    args, H, dk, dv, per_token, code, dev = _lin_inputs(q, k, v, g, "BT")
     B, T = q.shape[:2]
-    args, H, dk, dv, per_token, code, dev = _lin_inputs(q, k, v, g)
     args += (_arg(S0, "S0", F32, (B, H, dv, dk), dev, True), _arg(lens, "lens", I32, (B,), dev, True))
     o = _like(o, "o", v)
     if S_final is not None or return_final:
@@ -86,7 +86,7 @@ def lin_attn_fwd(q, k, v, g=None, S0=None, *, lens=None, o=None, S_final=None, r
 def lin_attn_step(S, q, k, v, g=None, *, o=None):
     """One token of linear attention: q, k [N,H,dk]; v [N,H,dv]; g [N,H] in q's dtype, [H] float32 or None;
     S [N,H,dv,dk] float32 updated in place.  Returns o [N,H,dv]."""
-    args, H, dk, dv, per_token, code, dev = _lin_inputs(q, k, v, g)
+    args, H, dk, dv, per_token, code, dev = _lin_inputs(q, k, v, g, "N")
     N = q.shape[0]
     S = _arg(S, "S", F32, (N, H, dv, dk), dev)
     o = _like(o, "o", v)
@@ -103,8 +103,8 @@ def lin_attn_bwd_workspace_bytes(B, T, H, dk, dv, dtype) -> int:
 def lin_attn_bwd(q, k, v, g, S0, dO, dS_final=None, *, lens=None, want_dS0=True, workspace=None):
     """Backward of lin_attn_fwd: gradients of sum(dO * o) + sum(dS_final * S_final).  Returns a dict dq, dk, dv,
     dg (None unless g has a decay for each token), dS0 (None unless want_dS0)."""
+    args, H, dk, dv, per_token, code, dev = _lin_inputs(q, k, v, g, "BT")
     B, T = q.shape[:2]
-    args, H, dk, dv, per_token, code, dev = _lin_inputs(q, k, v, g)
     args += (_arg(S0, "S0", F32, (B, H, dv, dk), dev, True), _arg(lens, "lens", I32, (B,), dev, True),
              _arg(dO, "dO", q.dtype, (B, T, H, dv), dev), _arg(dS_final, "dS_final", F32, (B, H, dv, dk), dev, True))
     r = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),

@@ -775,6 +775,20 @@ def test_the_binding_refuses(qd):
         qd.win_attn_fwd(q[0], q[0], v[0], window=4)
 
 
+@pytest.mark.parametrize("form,lead,wrong", [
+    ("fwd", "B, T", (100,)), ("fwd", "B, T", (2, 3, 5)), ("fwd", "B, T", ()),
+    ("bwd", "B, T", (100,)), ("bwd", "B, T", (2, 3, 5)),
+    ("step", "N", (2, 5)), ("step", "N", ()),
+])
+def test_linear_attention_refuses_other_ranks(qd, form, lead, wrong):
+    """One sequence without its batch dimension, several leading dimensions: sizes taken from them would be others'."""
+    q, S = torch.zeros(*wrong, 8, 64, dtype=BF16), torch.zeros(2, 8, 64, 64)
+    call = {"fwd": lambda: qd.lin_attn_fwd(q, q, q), "bwd": lambda: qd.lin_attn_bwd(q, q, q, None, None, q),
+            "step": lambda: qd.lin_attn_step(S, q, q, q)}[form]
+    with pytest.raises(ValueError, match=rf"expected \[{lead}, H, d\]"):
+        call()
+
+
 @pytest.mark.gpu
 def test_the_binding_refuses_on_the_gpu(qd):
     x = lambda *s, dt=BF16: torch.zeros(*s, dtype=dt, device="cuda")
