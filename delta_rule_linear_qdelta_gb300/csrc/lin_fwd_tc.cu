@@ -49,11 +49,12 @@ constexpr uint32_t TM_A = 0, TM_O = 128, TM_DS = 256, TM_X = 384;
 struct Params {
     const void *g;
     const int *lens;
-    const float *first_state, *entering;      // of the first segment walked; of the others (null: zero)
+    const float *first_state, *entering;      // of a stream in one piece (null: zero); of the segments of the others
     float *last_state, *leaving, *decay;      // of the last one; of the others, with their decays (null: not written)
     uint8_t *chk;                             // states entering the chunks (leaving ones' gradients), as operand tiles
     void *o;
-    // segments: walked by a stream's CTAs here, in all, their chunks; states between them (`joints` a stream), `pieces` to a segment
+    // segments: walked by a stream's CTAs here, in all, their chunks; states that end one of the first pass (`joints` a stream: with
+    // the first, joints + 1 entering ones), `pieces` to a segment
     int g_token, T, H, nk, nv, walked, segs, seg_chunks, joints, pieces, back;
 };
 
@@ -367,8 +368,8 @@ lin_tc_kernel(const __grid_constant__ Params there, const __grid_constant__ Para
         const bool mine = row < DV, real_row = row < p.nv;
         float S[SC];
         {
-            const float *from = w == 0 ? p.first_state : p.entering;
-            if (from) from += ((w == 0 ? (size_t)bh : (size_t)bh * p.joints + w * p.pieces - 1) * p.nv + row) * p.nk;
+            const float *from = p.entering ? p.entering : p.first_state;
+            if (from) from += ((p.entering ? (size_t)bh * (p.joints + 1) + w * p.pieces : (size_t)bh) * p.nv + row) * p.nk;
 #pragma unroll
             for (int c = 0; c < SC; c += 4) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -481,7 +482,7 @@ lin_tc_kernel(const __grid_constant__ Params there, const __grid_constant__ Para
         if (!bar.abort && real_row) {
             float *to = w == p.segs - 1 ? p.last_state : p.leaving;
             if (to) {
-                to += ((w == p.segs - 1 ? (size_t)bh : (size_t)bh * p.joints + w) * p.nv + row) * p.nk + SC * half;
+                to += ((w == p.segs - 1 ? (size_t)bh : (size_t)bh * (p.joints + 1) + w + 1) * p.nv + row) * p.nk + SC * half;
 #pragma unroll
                 for (int c = 0; c < SC; c += 4)
                     if (SC * half + c < p.nk) *reinterpret_cast<float4 *>(to + c) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
@@ -516,18 +517,21 @@ lin_tc_kernel(const __grid_constant__ Params there, const __grid_constant__ Para
     if (warp == 0) tmem_dealloc(tm, 512);
 }
 
-// The states that enter the segments, in the place of the segments' own: S <- a_w S + own_w, walked in order.  A row of the grid
-// is a stream of one direction.
-__global__ void lin_join_kernel(const float *first_there, const float *first_back, float *own, const float *decay, int joints, int elements,
+// The states that enter the segments: the first one, which the last pass reads here alone (the state that leaves may have its
+// place, and nothing orders the CTAs of a stream's first and last segment), then, in the place of the segments' own,
+// S <- a_w S + own_w, walked in order.  A row of the grid is a stream of one direction.
+__global__ void lin_join_kernel(const float *first_there, const float *first_back, float *states, const float *decay, int joints, int elements,
                                 int streams) {
     const size_t row = blockIdx.y, bh = row % streams;
     const float *first = row < streams ? first_there : first_back;
     const int e = 4 * (blockIdx.x * blockDim.x + threadIdx.x);
     if (e >= elements) return;
     float4 S = first ? *reinterpret_cast<const float4 *>(first + bh * elements + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    states += row * (joints + 1) * elements + e;
+    *reinterpret_cast<float4 *>(states) = S;
 #pragma unroll 4
     for (int w = 0; w < joints; ++w) {
-        float4 *at = reinterpret_cast<float4 *>(own + (row * joints + w) * elements + e);
+        float4 *at = reinterpret_cast<float4 *>(states + (size_t)(w + 1) * elements);
         const float a = decay[row * joints + w];
         float4 v = *at;
         if (a != 0.f) v = make_float4(fmaf(a, S.x, v.x), fmaf(a, S.y, v.y), fmaf(a, S.z, v.z), fmaf(a, S.w, v.w));
@@ -582,7 +586,8 @@ cudaError_t walk(Walks &w, bool out, float *ws, cudaStream_t s, int *n) {
     const int ways = out ? 1 : 2;
     const Cut cut = cut_of((long long)ways * w.streams, w.p[0].T);
     const int joints = (cut.segs - 1) * cut.pieces, elements = w.p[0].nk * w.p[0].nv;
-    float *own = ws, *decay = ws + (size_t)ways * w.streams * joints * elements;
+    const size_t each = (size_t)w.streams * (joints + 1) * elements;     // of one direction
+    float *states = ws, *decay = ws + ways * each;
     if (joints) {
         Walks local = w;
         for (int d = 0; d < 2; ++d) {
@@ -592,14 +597,14 @@ cudaError_t walk(Walks &w, bool out, float *ws, cudaStream_t s, int *n) {
             p.walked = p.joints = joints;
             p.first_state = p.entering = nullptr;
             p.last_state = nullptr;
-            p.leaving = own + (size_t)d * w.streams * joints * elements;
+            p.leaving = states + d * each;
             p.decay = decay + (size_t)d * w.streams * joints;
             p.chk = nullptr;
         }
         cudaError_t e = launch<false>(local, s, n, ways * w.streams * joints);   // (one way: without the other's CTAs)
         if (e != cudaSuccess) return e;
         lin_join_kernel<<<dim3((unsigned)((elements / 4 + 255) / 256), (unsigned)(ways * w.streams)), 256, 0, s>>>(
-            w.p[0].first_state, w.p[1].first_state, own, decay, joints, elements, w.streams);
+            w.p[0].first_state, w.p[1].first_state, states, decay, joints, elements, w.streams);
         *n += 1;
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -610,7 +615,7 @@ cudaError_t walk(Walks &w, bool out, float *ws, cudaStream_t s, int *n) {
         p.seg_chunks = cut.chunks;
         p.joints = joints;
         p.pieces = cut.pieces;
-        p.entering = joints ? own + (size_t)d * w.streams * joints * elements : nullptr;
+        p.entering = joints ? states + d * each : nullptr;
     }
     return out ? launch<true>(w, s, n, w.streams * cut.segs) : launch<false>(w, s, n, 2 * w.streams * cut.segs);
 }
@@ -627,8 +632,8 @@ Params params_of(const LinArgs &a) {
 size_t lin_tc_workspace(int B, int T, int H, int nk, int nv, int ways) {
     const size_t walks = (size_t)ways * B * H;
     const Cut cut = cut_of(walks, T);
-    const size_t joints = walks * (cut.segs - 1) * cut.pieces;
-    return (joints * nk * nv + joints) * sizeof(float);
+    const size_t joints = (size_t)(cut.segs - 1) * cut.pieces;
+    return joints ? walks * ((joints + 1) * nk * nv + joints) * sizeof(float) : 0;
 }
 
 cudaError_t launch_lin_fwd_tc(const LinArgs &a, cudaStream_t s, int *n) {

@@ -250,6 +250,23 @@ def test_a_prompt_in_pieces_and_tokens_is_the_whole(qd, dt):
     close(S, want[1], mag[1], "S")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("B,T,H,lens", [(1, 8192, 2, None), (3, 2000, 5, [2000, 130, 0]), (2, 897, 38, [1, 897]), (1, 40000, 1, [200])])
+def test_a_state_carried_in_place_through_long_sequences(qd, B, T, H, lens, dt):
+    """S_final over S0 where a sequence is cut into segments, some of them of padding alone: as in a buffer of its own."""
+    d = lin_inputs(B, T, H, 64, 128, dt, T + H, "token", True)
+    c = cu(d)
+    n = None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda()
+    o, S = qd.lin_attn_fwd(c["q"], c["k"], c["v"], c["g"], c["S0"], lens=n)
+    for _ in range(3):
+        carried = c["S0"].clone()
+        again, end = qd.lin_attn_fwd(c["q"], c["k"], c["v"], c["g"], carried, lens=n, S_final=carried)
+        assert end is carried and torch.equal(carried, S) and torch.equal(again, o)
+    if lens is not None and 0 in lens:
+        assert torch.equal(S[lens.index(0)], c["S0"][lens.index(0)])
+
+
 def chunked(q, k, v, g, S0, C=128):
     """Linear attention in 64 bits by chunks, for long sequences on the GPU: [T,d] q, k, v, [T] g, one head."""
     S, o = S0.clone(), []
