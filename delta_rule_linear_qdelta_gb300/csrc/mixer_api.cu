@@ -206,7 +206,6 @@ qd_status win_attn_fill(void *K, void *V, const void *k, const void *v, const in
     const Named args[] = {{"K", K, key}, {"V", V, key}, {"k", k, key}, {"v", v, key}, {"lens", lens, false}};
     QD_CHECK_POINTERS(fn, args);
     if (!key) return qd::end_call(0);
-    if ((double)B * ((double)window + sinks) * Hkv * d / 8 > 256 * kMostCtas) return fail(QD_ERR_ARG, "%s: sizes overflow", fn);
     qd::WinArgs a{};
     a.k = k; a.v = v; a.lens = lens; a.K = K; a.V = V;
     a.B = B; a.T = T; a.past = past; a.H = Hkv; a.Hkv = Hkv; a.d = d; a.window = window; a.sinks = sinks;

@@ -400,10 +400,12 @@ template <int DP> cudaError_t run_step(const WinArgs &a, const Plan &p, int dtyp
 // 16 bytes a thread; slots without a token are left as they are.
 template <typename T> __global__ void win_fill_kernel(WinArgs a) {
     constexpr int VEC = 16 / sizeof(T);
-    const int slots = a.sinks + a.window, per_row = a.Hkv * a.d / VEC;
+    const int slots = a.sinks + a.window;
+    const size_t row = (size_t)a.Hkv * a.d, per_row = row / VEC;          // (row: up to 2^36 elements)
     const size_t u = (size_t)blockIdx.x * blockDim.x + threadIdx.x, all = (size_t)a.B * slots * per_row;
     if (u >= all) return;
-    const int b = (int)(u / ((size_t)slots * per_row)), s = (int)(u / per_row % slots), c = (int)(u % per_row) * VEC;
+    const int b = (int)(u / (slots * per_row)), s = (int)(u / per_row % slots);
+    const size_t c = u % per_row * VEC;
     const int n = a.past + real_tokens(a.lens, b, a.T);
     int p = s;
     if (s >= a.sinks && n > slots) {                        // the last token whose slot this is
@@ -411,7 +413,7 @@ template <typename T> __global__ void win_fill_kernel(WinArgs a) {
         p = a.sinks + count - 1 - (count - 1 - r) % a.window;
     }
     if (p >= n) return;
-    const size_t from = ((size_t)b * (a.past + a.T) + p) * a.Hkv * a.d + c, to = ((size_t)b * slots + s) * a.Hkv * a.d + c;
+    const size_t from = ((size_t)b * (a.past + a.T) + p) * row + c, to = ((size_t)b * slots + s) * row + c;
     Pack<T, VEC> x, y;
     x.load(static_cast<const T *>(a.k) + from);
     y.load(static_cast<const T *>(a.v) + from);
@@ -442,7 +444,7 @@ cudaError_t launch_win_step(const WinArgs &a, int dtype, cudaStream_t s, int *n)
 }
 
 cudaError_t launch_win_fill(const WinArgs &a, int dtype, cudaStream_t s, int *n) {
-    const size_t vec = dtype == kBF16 ? 8 : 4, all = (size_t)a.B * (a.sinks + a.window) * (a.Hkv * a.d / vec);
+    const size_t vec = dtype == kBF16 ? 8 : 4, all = (size_t)a.B * (a.sinks + a.window) * ((size_t)a.Hkv * a.d / vec);
     const unsigned grid = (unsigned)((all + 255) / 256);
     if (dtype == kBF16) win_fill_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
     else win_fill_kernel<float><<<grid, 256, 0, s>>>(a);

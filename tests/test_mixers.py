@@ -482,6 +482,24 @@ def test_a_cache_from_a_prompt_goes_on_as_the_prompt_would(qd, window, sinks, pa
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,window,sinks,T", [(1 << 24, 1, 0, 2), ((1 << 24) + 8, 1, 0, 1), (16, 1 << 20, 40, (1 << 20) + 100)])
+def test_a_cache_whose_rows_or_whole_pass_32_bits(qd, heads, window, sinks, T):
+    """A token's keys of 2^31 elements and more, and a cache of so many."""
+    d, slots = 128, window + sinks
+    K, V = (torch.zeros(1, slots, heads, d, dtype=BF16, device="cuda") for _ in range(2))
+    k, v = (torch.randn(1, T, heads, d, dtype=BF16, device="cuda", generator=torch.Generator("cuda").manual_seed(i)) for i in range(2))
+    qd.win_attn_fill(K, V, k, v, window=window, sinks=sinks)
+    for cache, new in ((K, k), (V, v)):
+        for p in range(T) if T < 4 else (0, sinks - 1, T - slots + sinks, T - 100, T - 1):
+            at = p if p < slots else sinks + (p - sinks) % window
+            if p < sinks or p >= T - window:
+                assert torch.equal(cache[0, at], new[0, p]), p
+    if T > 4:                                           # every slot behind the sinks: the ring, turned
+        turned = torch.roll(k[0, T - window:], (T - sinks) % window, 0)
+        assert torch.equal(K[0, sinks:], turned)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_a_prompt_in_pieces(qd, dt):
     """A piece's kept keys are the sinks' and the last window - 1."""
