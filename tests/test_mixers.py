@@ -306,6 +306,97 @@ def test_long_sequences_of_few_heads(qd, T, n, dt):
             assert rel <= t, (name, rel)
 
 
+def chunked_batch(q, k, v, g, S0, C=128):
+    """The same in 64 bits for a batch of heads, q, k, v [N,T,d], g [N,T] or None, S0 [N,dv,dk]; decays below -87 drop the
+    state.  Exponents of pairs that do not see each other never enter an exponential."""
+    N, T, _ = q.shape
+    g = torch.zeros(N, T, dtype=q.dtype, device=q.device) if g is None else g
+    drop = g < -87
+    g = torch.where(drop, torch.zeros_like(g), g)
+    if S0 is None:
+        S0 = torch.zeros(N, v.shape[-1], q.shape[-1], dtype=q.dtype, device=q.device)
+    zero, S, o = torch.zeros((), dtype=q.dtype, device=q.device), S0, []
+    weight = lambda x, see: torch.where(see, torch.exp(torch.where(see, x, zero)), zero)
+    for t in range(0, T, C):
+        qc, kc, vc, P, piece = q[:, t:t + C], k[:, t:t + C], v[:, t:t + C], torch.cumsum(g[:, t:t + C], 1), drop[:, t:t + C].cumsum(1)
+        n = P.shape[1]
+        see = torch.ones(n, n, dtype=torch.bool, device=q.device).tril() & (piece[:, :, None] == piece[:, None])
+        M = weight(P[:, :, None] - P[:, None], see)
+        o.append(((qc @ kc.mT) * M) @ vc + weight(P, piece == 0)[..., None] * (qc @ S.mT))
+        S = weight(P[:, -1], piece[:, -1] == 0)[:, None, None] * S + (weight(P[:, -1:] - P, piece == piece[:, -1:])[..., None] * vc).mT @ kc
+    return torch.cat(o, 1), S
+
+
+def chunked_bwd(d, lens):
+    """Gradients in 64 bits as ref.lin_bwd's, sequence by sequence, on the GPU; padded tokens' are 0."""
+    B, T, H, _ = d["q"].shape
+    names = [x for x in ("q", "k", "v", "g", "S0") if d[x] is not None]
+    out = {"d" + x: torch.zeros(d[x].shape, dtype=F64) for x in names}
+    for b, n in enumerate(ref.lens_list(lens, B, T)):
+        if n == 0:
+            out["dS0"][b] = d["dS_final"][b]
+            continue
+        heads = lambda x: d[x][b] if x == "S0" else d[x][b, :n].transpose(0, 1)
+        leaf = {x: heads(x).cuda().contiguous().requires_grad_() for x in names}
+        o, S = chunked_batch(*(leaf.get(x) for x in ("q", "k", "v", "g", "S0")))
+        loss = (o * heads("dO").cuda()).sum() + (S * d["dS_final"][b].cuda()).sum()
+        for x, t in zip(names, torch.autograd.grad(loss, list(leaf.values()))):
+            if x == "S0":
+                out["dS0"][b] = t.cpu()
+            else:
+                out["d" + x][b, :n] = t.transpose(0, 1).cpu()
+    return out
+
+
+def test_the_chunked_definition_is_the_definition():
+    d = dropped(wide(lin_inputs(2, 140, 2, 16, 8, F32, 31, "drop")))
+    o, S = ref.lin_fwd(*(d[x] for x in ("q", "k", "v", "g", "S0")))
+    for b in range(2):
+        got = chunked_batch(*(d[x][b].transpose(0, 1) for x in ("q", "k", "v", "g")), d["S0"][b])
+        assert torch.allclose(got[0].transpose(0, 1), o[b], rtol=1e-12, atol=1e-12)
+        assert torch.allclose(got[1], S[b], rtol=1e-12, atol=1e-12)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (128, 40), (24, 128)])
+@pytest.mark.parametrize("decays", ["mixed", "none"])
+def test_linear_attention_gradients_of_many_chunks(qd, decays, dk, dv, dt):
+    """More chunks than the GPU has SMs twice over, so that each CTA takes several in turn: whole, cut by padding and all
+    padding ones, chunks whose decays are weak, strong and drop the state side by side.  The same bits every time."""
+    B, T, H = 4, 1200, 16
+    x = lin_inputs(B, T, H, dk, dv, dt, dk + dv, "none")
+    g = torch.Generator().manual_seed(5)
+    n = torch.tensor([1300, 1, 700, 1100], dtype=torch.int32)
+    assert H * sum(-(-min(m, T) // 128) for m in n.tolist()) > 2 * 152
+    for y in ("q", "k", "v", "dO"):
+        poison(x[y], n)
+    x["lens"] = n
+    if decays == "mixed":
+        ld = -torch.nn.functional.softplus(0.5 * torch.randn(B, T, H, generator=g) - 4)
+        kind = torch.randint(0, 4, (B, -(-T // 128), H), generator=g).repeat_interleave(128, 1)[:, :T]   # a chunk's: weak, weak, strong, drops
+        ld = torch.where((kind == 2) & (torch.rand(B, T, H, generator=g) < 0.3), -20 * torch.rand(B, T, H, generator=g), ld)
+        ld = torch.where((kind == 3) & (torch.rand(B, T, H, generator=g) < 0.05), torch.full((), -INF), ld)
+        x["g"] = poison(ld.to(dt), n)
+    w, c = dropped(wide(x)), cu(x)
+    run = lambda: qd.lin_attn_bwd(c["q"], c["k"], c["v"], c["g"], c["S0"], c["dO"], c["dS_final"], lens=c["lens"])
+    got = run()
+    want, mag = (chunked_bwd(e, n) for e in (w, mags(w)))
+    if decays == "none":
+        assert got.pop("dg") is None
+    assert set(got) == set(want)
+    for y in want:
+        close(got[y], want[y], mag[y], y, extra=decay_noise(w, mag) if y == "dg" else 0.0)
+        # random signs: the relative error is of one rounding's size, of up to four that are independent (root mean square
+        # 2^-8 / sqrt 3 at most)
+        if got[y].dtype == BF16:
+            rel = float((got[y].cpu().double() - want[y]).norm() / want[y].norm())
+            assert rel <= 5e-3, (y, rel)
+    for _ in range(5):
+        again = run()
+        assert all(torch.equal(again[y], got[y]) for y in want)
+
+
 # ------------------------------------------------------------------ windowed attention
 
 def win_inputs(B, T, past, H, Hkv, d, dt, seed, lens=False):
