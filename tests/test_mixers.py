@@ -503,6 +503,75 @@ def test_scores_of_any_size(qd, scale, far, dt):
     assert ((lse.cpu().double() - z).abs() <= off + 1e-5 * (1 + z.abs())).all()
 
 
+def bwd_terms(q, k, v, dO, window, sinks, scale):
+    """For dq, dk, dv of one sequence [T,H,d]: the sum over the terms of what a relative error of each probability can move
+    (D among it: the sum of all of the row's), in units of that error."""
+    r = q.shape[1] // k.shape[1]
+    kr, vr = (t.repeat_interleave(r, 1).abs() for t in (k, v))
+    P, _ = ref.win_probs(q, k, window, sinks, scale)
+    dP = torch.einsum("thd,shd->hts", dO.abs(), vr)
+    dS = P * (dP + (P * dP).sum(-1, keepdim=True))
+    fold = lambda t: t.unflatten(1, (-1, r)).sum(2)
+    return {"dq": abs(scale) * torch.einsum("hts,shd->thd", dS, kr), "dk": fold(abs(scale) * torch.einsum("hts,thd->shd", dS, q.abs())),
+            "dv": fold(torch.einsum("hts,thd->shd", P, dO.abs()))}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("scale,far", [(1.0, 60.0), (20.0, 3.0), (0.0, 1.0), (-0.2, 1.0)])
+@pytest.mark.parametrize("T,H,window,sinks", [(150, 2, 50, 2), (700, 2, 50, 5), (400, 8, 1 << 30, 0)])
+def test_gradients_with_scores_of_any_size(qd, T, H, window, sinks, scale, far, dt):
+    """As above for the backward: one walk a key tile, sinks in slices, walks in pieces."""
+    d = 64
+    x = win_inputs(1, T, 0, H, 1, d, dt, 3)
+    x["q"] = (far * x["q"].float()).to(dt)
+    c, w, kw = cu(x), wide(x), {"window": window, "sinks": sinks, "scale": scale}
+    if T > 150:                                         # parts beside the rows' D
+        assert qd.win_attn_bwd_workspace_bytes(1, T, 0, H, 1, d, window, sinks, qd.QD_BF16 if dt == BF16 else qd.QD_F32) > 4 * T * H + 256
+    o, lse = qd.win_attn_fwd(c["q"], c["k"], c["v"], **kw)
+    got = qd.win_attn_bwd(c["q"], c["k"], c["v"], o, lse, c["dO"], **kw)
+    want, mag = ref.win_bwd(w["q"], w["k"], w["v"], w["dO"], window, sinks, scale)
+    terms = bwd_terms(*(w[y][0] for y in ("q", "k", "v", "dO")), window, sinks, scale)
+    # a score is a sum of 64 products, whose 64 roundings of 2^-24 of the sum of their sizes have random signs; a
+    # probability's exponent has its own, the one in lse, and lse's own rounding and product, each no larger
+    size = abs(scale) * torch.einsum("thd,sd->hts", w["q"][0].abs(), w["k"][0, :, 0].abs()).max()
+    off = 3 * 8 * 2.0 ** -24 * float(size)
+    for y in want:
+        g, m = got[y].cpu().double(), mag[y].abs()
+        assert torch.isfinite(g).all(), y
+        # roundings to bf16 as everywhere here: the probability's gradient, the o that enters it, the output
+        over = (g - want[y]).abs() - (3 * HALF if dt == BF16 else 0) * m - (off + 1e-5) * terms[y][None] - 1e-5 * (m + want[y].abs().max())
+        assert over.max() <= 0, (y, float(over.max()))
+        if scale == 0 and y != "dv":
+            assert (g == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [False, True])
+def test_keys_beyond_what_stays_in_l2(qd, lens):
+    """A batch whose windows' keys are more than 64 MB takes its query blocks in another order than its sequences alone do:
+    the same bits."""
+    B, T, past, H, d, window, sinks = 16, 640, 33, 16, 128, 600, 4
+    g = torch.Generator("cuda").manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF16)
+    q, k, v, dO = r(B, T, H, d), r(B, past + T, H, d), r(B, past + T, H, d), r(B, T, H, d)
+    assert 4 * B * H * d * window > 64e6 > 4 * H * d * window
+    n = torch.randint(0, T + 1, (B,), dtype=torch.int32, device="cuda", generator=g) if lens else None
+    kw = {"window": window, "sinks": sinks}
+    o, lse = qd.win_attn_fwd(q, k, v, lens=n, **kw)
+    got = qd.win_attn_bwd(q, k, v, o, lse, dO, lens=n, **kw)
+    for b in range(B):
+        one, m = (lambda t: t[b:b + 1]), None if n is None else n[b:b + 1]
+        o1, lse1 = qd.win_attn_fwd(one(q), one(k), one(v), lens=m if m is None else m.clone(), **kw)
+        assert torch.equal(o1, one(o)) and torch.equal(lse1, one(lse))
+        r1 = qd.win_attn_bwd(one(q), one(k), one(v), o1, lse1, one(dO), lens=m if m is None else m.clone(), **kw)
+        assert torch.equal(r1["dq"], one(got["dq"]))
+        for y in ("dk", "dv"):                          # (walks may be cut otherwise: sums in fp32, rounded once)
+            a, z = one(got[y]).float(), r1[y].float()
+            assert (a - z).abs().max() <= 2 * HALF * z.abs().max()
+            assert (a - z).norm() <= 1e-3 * z.norm()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("N,H,Hkv,d,window,sinks", [(1, 1, 1, 8, 1, 0), (3, 4, 2, 128, 33, 4), (2, 16, 1, 64, 200, 1),
@@ -632,6 +701,89 @@ def test_sinks_of_a_long_sequence(qd, dt, tol):
         assert rel(got["d" + y][0], b) <= tol, y
         if y != "q":
             assert rel(got["d" + y][0, :sinks], b[:sinks]) <= tol, y
+
+
+# ------------------------------------------------------------------ arrays beyond 2^31 elements
+
+def _first_and_last(small, n):
+    """[2, ...] as the first and the last of n, zeros between."""
+    big = torch.zeros(n, *small.shape[1:], dtype=small.dtype, device="cuda")
+    big[0], big[-1] = small[0], small[1]
+    return big
+
+
+def _same_at_the_ends(big, small):
+    assert torch.equal(big[0], small[0]) and torch.equal(big[-1], small[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt,H,d", [(BF16, 16, 128), (F32, 128, 16)])
+def test_linear_attention_of_arrays_beyond_32_bits(qd, dt, H, d):
+    """Sequences that are not cut: the first and the last of a batch as in a batch of two, nothing in the others."""
+    B, T = 2049, 512
+    assert B * T * H * d > 1 << 31
+    c = cu(lin_inputs(2, T, H, d, d, dt, 1, "token"))
+    x = {y: _first_and_last(c[y], B) for y in ("q", "k", "v", "g", "S0", "dO", "dS_final")}
+    o, S = qd.lin_attn_fwd(x["q"], x["k"], x["v"], x["g"], x["S0"])
+    want = qd.lin_attn_fwd(c["q"], c["k"], c["v"], c["g"], c["S0"])
+    _same_at_the_ends(o, want[0])
+    _same_at_the_ends(S, want[1])
+    assert not o[1:-1].any() and not S[1:-1].any()
+    del o, S
+    got = qd.lin_attn_bwd(x["q"], x["k"], x["v"], x["g"], x["S0"], x["dO"], x["dS_final"])
+    want = qd.lin_attn_bwd(c["q"], c["k"], c["v"], c["g"], c["S0"], c["dO"], c["dS_final"])
+    for y in want:
+        _same_at_the_ends(got[y], want[y])
+        assert not got[y][1:-1].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt,H,d,sinks", [(BF16, 16, 128, 3), (F32, 128, 16, 0)])
+def test_windowed_attention_of_arrays_beyond_32_bits(qd, dt, H, d, sinks):
+    B, T, kw = 2049, 512, {"window": 100, "sinks": sinks}
+    c = cu(win_inputs(2, T, 0, H, H, d, dt, 1))
+    x = {y: _first_and_last(c[y], B) for y in ("q", "k", "v", "dO")}
+    o, lse = qd.win_attn_fwd(x["q"], x["k"], x["v"], **kw)
+    o2, lse2 = qd.win_attn_fwd(c["q"], c["k"], c["v"], **kw)
+    _same_at_the_ends(o, o2)
+    _same_at_the_ends(lse, lse2)
+    assert not o[1:-1].any()
+    got = qd.win_attn_bwd(x["q"], x["k"], x["v"], o, lse, x["dO"], **kw)
+    want = qd.win_attn_bwd(c["q"], c["k"], c["v"], o2, lse2, c["dO"], **kw)
+    for y in want:
+        _same_at_the_ends(got[y], want[y])
+        assert not got[y][1:-1].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_steps_of_states_and_caches_beyond_32_bits(qd, dt):
+    N, H, d = 8193, 16, 128
+    c = cu(lin_inputs(2, 1, H, d, d, dt, 1, "token"))
+    x = {y: _first_and_last(c[y] if y == "S0" else c[y][:, 0].contiguous(), N) for y in ("q", "k", "v", "g", "S0")}
+    assert x["S0"].numel() > 1 << 31
+    o = qd.lin_attn_step(x["S0"], x["q"], x["k"], x["v"], x["g"])
+    S = c["S0"].clone()
+    _same_at_the_ends(o, qd.lin_attn_step(S, *(c[y][:, 0].contiguous() for y in ("q", "k", "v", "g"))))
+    _same_at_the_ends(x["S0"], S)
+    del x, o
+    N, H, Hkv, window, sinks = 4, 8, 4, 1 << 20, 3
+    g = torch.Generator("cuda").manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=dt)
+    K, V = (torch.zeros(N, window + sinks, Hkv, d, dtype=dt, device="cuda") for _ in range(2))
+    assert K.numel() > 1 << 31
+    K[-1], V[-1] = r(window + sinks, Hkv, d), r(window + sinks, Hkv, d)
+    q, k, v = r(N, H, d), r(N, Hkv, d), r(N, Hkv, d)
+    p = 5 * window + 77
+    o = qd.win_attn_step(K, V, torch.full((N,), p, dtype=torch.int32, device="cuda"), q, k, v, window=window, sinks=sinks)
+    at = sinks + (p - sinks) % window
+    assert torch.equal(K[-1, at], k[-1]) and torch.equal(V[-1, at], v[-1]) and torch.equal(K[0, at], k[0])
+    # relative L2 over a million keys: errors of random signs, of one rounding's size each (the probability's, the output's)
+    for h in range(H):
+        s = (K[-1, :, h // 2].double() @ q[-1, h].double()) / math.sqrt(d)
+        want = torch.softmax(s, 0) @ V[-1, :, h // 2].double()
+        rel = float((o[-1, h].double() - want).norm() / want.norm())
+        assert rel <= (5e-3 if dt == BF16 else 1e-5), (h, rel)
 
 
 # ------------------------------------------------------------------ how they are called
