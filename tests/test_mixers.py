@@ -843,6 +843,27 @@ def test_the_same_inputs_give_the_same_bits_on_any_stream(qd):
 
 
 @pytest.mark.gpu
+def test_calls_on_two_streams_at_once(qd):
+    """Every call on one stream while the others run on another: the same bits as alone."""
+    calls = list(_calls(qd))
+    alone = [call(d) for d, call in calls]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for i in range(len(calls)):                     # (the second stream takes them from the other end)
+            for s, at, out in zip(streams, (i, len(calls) - 1 - i), got):
+                with torch.cuda.stream(s):
+                    out.append((at, calls[at][1](calls[at][0])))
+    torch.cuda.synchronize()
+    for at, out in got[0] + got[1]:
+        for a, b in zip(out, alone[at]):
+            assert (a is None and b is None) or torch.equal(a, b)
+    assert qd.qd_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_captured_and_replayed(qd):
     """A call captured into a graph and replayed on new inputs gives what a direct call gives."""
     for d, call in _calls(qd):
