@@ -13,11 +13,12 @@
 //         (the other).  TMEM: S^T 0-127, dP^T 128-255, dV 256-383, dK 384-511.
 //
 // Tiles of sinks are seen by every later query: those beyond the tile's window are cut into slices of their own CTAs, which
-// leave fp32 parts of the sinks' rows to be summed in order (win_sinks_kernel).  Walks that are long for the number of SMs are
+// leave fp32 parts of the sinks' rows to be summed in order (win_sinks_kernel); more than two tiles of sinks are not cut.  Walks that are long for the number of SMs are
 // cut into pieces, summed likewise (win_pieces_kernel).
 //
-// Bound by the tensor core: 14 d flop a pair of the tiles.  4 x 4096 tokens, 8 heads on 2, window 1024, 4 sinks: dq 113 us,
-// dk dv 127, the sinks' sums 3 (608 TFLOP/s of the 10 d a pair that is seen; tensor cores active 47 and 64 %).
+// Bound by the tensor core: 14 d flop a pair of the tiles.  4 x 4096 tokens, 8 heads on 2, window 1024, 4 sinks: 253 us (597
+// TFLOP/s of the 10 d a pair that is seen), of which under a profiler dq has 115, dk dv 132, the sinks' sums 6; tensor cores
+// active 47 and 64 %.
 //
 // Every wait is bounded; on a timeout the kernel sets its error word, waits (bounded) for its own copies and products,
 // frees TMEM and returns.
@@ -625,7 +626,9 @@ __global__ void win_pieces_kernel(Params p, __nv_bfloat16 *dk, __nv_bfloat16 *dv
 }
 
 // How the second kernel is cut.  Tiles of sinks: where the queries beyond the window outnumber the window's, as many slices
-// as leave each about a window's work (1: nothing is cut).  All tiles: where the longest walk, of the queries of a window and the
+// as leave each about a window's work (1: nothing is cut).  More than two such tiles are left whole, CTAs that walk every later
+// query, which is slow where the window is short: 1 x 32768 tokens, 16 heads on 4, window 512: 4 sinks 691 us, 256 795, 257
+// 2192.  All tiles: where the longest walk, of the queries of a window and the
 // heads that share the keys, is more than one and a half times an SM's share of all, into `near` pieces of about half a share, of
 // at least eight pairs of tiles; a kernel of its own adds the pieces up.  Both directions, us, without and with pieces:
 // 1 x 4096 tokens, 16 heads on 1, all keys: 867, 219; 2 x 4096, 16 on 2: 579, 423; 1 x 300, 16 on 1: 96, 41; a window of 2048 of
@@ -670,7 +673,7 @@ template <int DP> cudaError_t run(const WinArgs &a, cudaStream_t s, int *n) {
     if (e != cudaSuccess) return e;
     const Cut cut = cut_of(a.B, a.T, a.past, a.H, a.Hkv, a.window, a.sinks);
     // (dq's blocks together where the window does not make them alike: 1 x 8192 tokens, 8 heads on 8, all keys 418 us, 370 so; a window
-    // of 1024 of 4 x 4096 tokens 248, 251)
+    // of 1024 of 4 x 4096 tokens the same either way)
     Params p{a.lse, a.lens, static_cast<float *>(a.ws), nullptr, nullptr, a.B, a.T, a.past, a.H, a.Hkv, a.d, a.window, a.sinks,
              (a.T + kRows - 1) / kRows, (keys + kRows - 1) / kRows, cut.tiles, cut.slices, cut.near,
              2.0 * a.window > keys && blocks_together(a), a.scale};

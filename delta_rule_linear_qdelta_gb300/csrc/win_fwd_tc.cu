@@ -15,7 +15,7 @@
 //
 // Bound by the tensor core: 4 d flop a pair of a query and a key in the tiles, of which a window of W keys needs
 // W / (W + 128).  (A tile of up to 32 sinks is taken as one of 32 keys.)  Measured: 8 x 2048 tokens, 16 heads on 4, window 512, 4
-// sinks: 107 us (565 TFLOP/s of what is seen, 29 % of the measured rate); 1 x 32768, window 2048: 467 us (1.14 PFLOP/s, 59 %).
+// sinks: 107 us (565 TFLOP/s of what is seen, 29 % of the measured rate); 1 x 32768, window 2048: 468 us (1.14 PFLOP/s, 59 %).
 // At the first of them issue slots are 42 % busy, tensor cores 37 %, the exponential unit 20 %: what is left is the latency of
 // the chain scores, softmax, product over the five or six tiles of a CTA's walk, its start and its way out.
 //

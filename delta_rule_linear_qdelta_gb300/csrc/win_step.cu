@@ -251,7 +251,7 @@ template <int DP, int NQ> __global__ void __launch_bounds__(kThreads) win_step_m
                 c[n][e] = exp2_fast(c[n][e] - m[n][e & 1]);
                 l[n][e & 1] += c[n][e];
             }
-            b[n][0] = transpose8(pack2(c[n][0], c[n][1]));  // probabilities are held in bf16 (2^-9 each, as the values)
+            b[n][0] = transpose8(pack2(c[n][0], c[n][1]));  // probabilities are held in bf16 (half a step, 2^-8, as the values)
             b[n][1] = transpose8(pack2(c[n][2], c[n][3]));
         }
 #pragma unroll
@@ -369,7 +369,7 @@ template <int DP, int NQ> __global__ void __launch_bounds__(kThreads) win_step_f
 }
 
 // Queries of a CTA: 8 or 16 of bf16, up to 4 of fp32.  Slots are cut while the CTAs would leave SMs without
-// three of them (a CTA's four warps then still have four tiles of 16 slots each, or their groups as many rows).
+// three of them, at least 192 to a CTA but the last (three tiles of 16 for each of four warps, or twelve rows for each of 16 groups).
 int queries_of(int r, int dtype) { return dtype == kBF16 ? (r > 8 ? 16 : 8) : (r >= 4 ? 4 : r >= 2 ? 2 : 1); }
 Plan plan_of(int N, int H, int Hkv, int window, int sinks, int dtype) {
     const int r = H / Hkv, slots = window + sinks, least = 256;
