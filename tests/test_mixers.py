@@ -267,6 +267,30 @@ def test_a_state_carried_in_place_through_long_sequences(qd, B, T, H, lens, dt):
         assert torch.equal(S[lens.index(0)], c["S0"][lens.index(0)])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("a_token", [0.1, 0.31, 0.45, 0.49, 0.6])
+@pytest.mark.parametrize("power", [-56, -30, 30, 56])
+def test_linear_attention_of_small_and_large_values(qd, power, a_token, dt):
+    """Queries, and a loss, scaled by a power of two: outputs and gradients are linear in them, whatever the decays of a
+    chunk sum to.  All results are far inside the range of both types."""
+    d = lin_inputs(1, 200, 2, 64, 64, dt, 17, "token", True)
+    d["g"] = torch.full((1, 200, 2), -a_token).to(dt)
+    f = 2.0 ** power
+    fwd = {**d, "q": (d["q"].float() * f).to(dt)}
+    c, w = cu(fwd), wide(fwd)
+    o, S = qd.lin_attn_fwd(c["q"], c["k"], c["v"], c["g"], c["S0"])
+    want, mag = (ref.lin_fwd(*(e[x] for x in ("q", "k", "v", "g", "S0"))) for e in (w, mags(w)))
+    close(o, want[0], mag[0], "o")
+    close(S, want[1], mag[1], "S_final")
+    bwd = {**d, "dO": (d["dO"].float() * f).to(dt), "dS_final": d["dS_final"] * f}
+    c, w = cu(bwd), wide(bwd)
+    got = qd.lin_attn_bwd(c["q"], c["k"], c["v"], c["g"], c["S0"], c["dO"], c["dS_final"])
+    want, mag = (ref.lin_bwd(e) for e in (w, mags(w)))
+    for x in want:
+        close(got[x], want[x], mag[x], x, extra=decay_noise(w, mag) if x == "dg" else 0.0)
+
+
 def chunked(q, k, v, g, S0, C=128):
     """Linear attention in 64 bits by chunks, for long sequences on the GPU: [T,d] q, k, v, [T] g, one head."""
     S, o = S0.clone(), []
